@@ -41,6 +41,14 @@ STRATA_DECODE_MAX_TOKENS = 16
 STRATA_Q2_TILE_BYTES = 1280
 STRATA_Q4_TILE_BYTES = 2304
 STRATA_KV4_BLOCK = 32  # include/strata_kv.h
+# include/strata_attn.h
+STRATA_ROPE_HALF = 0
+STRATA_ROPE_INTERLEAVED = 1
+STRATA_ROPE_SCALE_NONE = 0
+STRATA_ROPE_SCALE_LINEAR = 1
+STRATA_ROPE_SCALE_NTK = 2
+STRATA_ROPE_SCALE_YARN = 3
+STRATA_ROPE_MAX_HEAD_DIM = 256
 FORMAT_OF_BITS = {2: STRATA_FMT_Q2_0_TILED, 4: STRATA_FMT_Q4_0_TILED}
 
 
@@ -50,13 +58,32 @@ class strata_moe_desc(ctypes.Structure):
                 ("weight_format", ctypes.c_int32), ("flags", ctypes.c_uint32), ("router_bias", ctypes.c_void_p)]
 
 
+class strata_rope_desc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_max_position", ctypes.c_int32), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("attn_factor", ctypes.c_double)]
+
+
+class strata_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class strata_kv4_attn_desc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("max_q_len", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_tokens", ctypes.c_int64), ("q_token_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class StrataError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{_lib.strata_status_string(status).decode()} ({status}): {msg}")
         self.status = status
 
 
-V, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+V, I32, SZ, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64
 DP = ctypes.POINTER(strata_moe_desc)
 _SIGS = {
     "strata_q2_matrix_bytes": (SZ, [I32, I32]),
@@ -87,6 +114,13 @@ _SIGS = {
     "strata_kv4_scale_bytes": (SZ, [ctypes.c_int64, I32]),
     "strata_kv4_encode": (I32, [V, ctypes.c_int64, I32, V, V, V]),
     "strata_kv4_decode": (I32, [V, V, ctypes.c_int64, I32, V, V]),
+    "strata_rope_create": (I32, [ctypes.POINTER(strata_rope_desc), ctypes.POINTER(V)]),
+    "strata_rope_destroy": (I32, [V]),
+    "strata_rope_apply": (I32, [V, V, I64, I64, V, I64, I32, V, I64, I64, V]),
+    "strata_kv4_append": (I32, [V, V, V, I64, V, I64, V, V, I64, V]),
+    "strata_kv4_copy_pages": (I32, [V, I32, V, V, I64, V]),
+    "strata_kv4_attention_workspace_bytes": (SZ, [V, I32]),
+    "strata_kv4_attention": (I32, [V, V, V, V, V, V, V, V, V, V, SZ, V]),
     "strata_status_string": (ctypes.c_char_p, [I32]),
     "strata_last_error": (ctypes.c_char_p, []),
 }
@@ -113,6 +147,19 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _host_i32(v):
+    """A host list of int32 as a CPU tensor (which keeps its memory) and its length."""
+    import torch
+    t = v if isinstance(v, torch.Tensor) else torch.as_tensor(v)
+    if t.device.type != "cpu" or t.dim() != 1 or (t.numel() and (t.is_floating_point() or t.is_complex())):
+        raise ValueError("page lists are one-dimensional host arrays of whole numbers")
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        if t.numel() and (int(t.max()) > 0x7fffffff or int(t.min()) < -0x80000000):
+            raise ValueError("page numbers are int32")
+        t = t.to(torch.int32).contiguous()
+    return t, t.numel()
 
 
 def _check(status: int):
@@ -216,6 +263,50 @@ def strata_kv4_encode(x, n_rows, head_dim, codes, scales, stream=None):
 def strata_kv4_decode(codes, scales, n_rows, head_dim, out, stream=None):
     """4-bit codes and fp16 scales of n_rows rows -> bf16 rows [n_rows, head_dim]."""
     _check(_lib.strata_kv4_decode(_ptr(codes), _ptr(scales), n_rows, head_dim, _ptr(out), _stream(stream)))
+
+
+def strata_rope_create(desc):
+    h = ctypes.c_void_p()
+    _check(_lib.strata_rope_create(ctypes.byref(desc), ctypes.byref(h)))
+    return h.value
+
+
+def strata_rope_destroy(rope):
+    _check(_lib.strata_rope_destroy(rope))
+
+
+def strata_rope_apply(rope, x, x_token_stride, x_head_stride, positions, n_tokens, n_heads, out, out_token_stride,
+                      out_head_stride, stream=None):
+    _check(_lib.strata_rope_apply(rope, _ptr(x), x_token_stride, x_head_stride, _ptr(positions), n_tokens, n_heads,
+                                  _ptr(out), out_token_stride, out_head_stride, _stream(stream)))
+
+
+def strata_kv4_append(cache, rope, k, k_token_stride, v, v_token_stride, positions, slots, n_tokens, stream=None):
+    _check(_lib.strata_kv4_append(ctypes.addressof(cache), rope, _ptr(k), k_token_stride, _ptr(v), v_token_stride,
+                                  _ptr(positions), _ptr(slots), n_tokens, _stream(stream)))
+
+
+def strata_kv4_copy_pages(caches, src, dst, stream=None):
+    """caches: a ctypes array of strata_kv4_cache (or a list of them); src, dst: host page lists (CPU int32
+    tensors, numpy arrays or sequences)."""
+    if not isinstance(caches, ctypes.Array):
+        caches = (strata_kv4_cache * len(caches))(*caches)
+    s, n = _host_i32(src)
+    d, m = _host_i32(dst)
+    if n != m:
+        raise ValueError(f"{n} source pages and {m} destinations")
+    _check(_lib.strata_kv4_copy_pages(ctypes.addressof(caches), len(caches), _ptr(s), _ptr(d), n, _stream(stream)))
+
+
+def strata_kv4_attention_workspace_bytes(cache, n_q_heads):
+    return _lib.strata_kv4_attention_workspace_bytes(ctypes.addressof(cache), n_q_heads)
+
+
+def strata_kv4_attention(cache, desc, rope, positions, q, q_offsets, kv_lens, block_table, out, workspace,
+                         workspace_bytes, stream=None):
+    _check(_lib.strata_kv4_attention(ctypes.addressof(cache), ctypes.addressof(desc), rope, _ptr(positions), _ptr(q),
+                                     _ptr(q_offsets), _ptr(kv_lens), _ptr(block_table), _ptr(out), _ptr(workspace),
+                                     workspace_bytes, _stream(stream)))
 
 
 def strata_rmsnorm_bf16(x, out, n_tokens, d, eps, stream=None):
@@ -348,3 +439,174 @@ class MoELayer:
 
     def pack_expert_device(self, gc, gs, uc, us, dc, ds, dst, stream=None):
         strata_moe_pack_expert_device(self.desc, gc, gs, uc, us, dc, ds, dst, stream)
+
+
+def _need(t, name, dtype, device=None):
+    """The entry points take raw pointers: refuse a tensor of another type or device than they will read."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}, not on {device if device is not None else 'a GPU'}")
+
+
+class Rope:
+    """Rotary positions of head rows: the table of frequencies (include/strata_attn.h)."""
+
+    LAYOUTS = {"half": STRATA_ROPE_HALF, "interleaved": STRATA_ROPE_INTERLEAVED}
+    SCALINGS = {"none": STRATA_ROPE_SCALE_NONE, "linear": STRATA_ROPE_SCALE_LINEAR, "ntk": STRATA_ROPE_SCALE_NTK,
+                "yarn": STRATA_ROPE_SCALE_YARN}
+
+    def __init__(self, head_dim, rotary_dim=None, theta=10000.0, layout="half", scaling="none", factor=1.0,
+                 original_max_position=0, beta_fast=0.0, beta_slow=0.0, attn_factor=0.0):
+        self.handle = None
+        self.head_dim = head_dim
+        self.desc = strata_rope_desc(head_dim, head_dim if rotary_dim is None else rotary_dim,
+                                     self.LAYOUTS.get(layout, -1), self.SCALINGS.get(scaling, -1), theta, factor,
+                                     original_max_position, beta_fast, beta_slow, attn_factor)
+        self.handle = strata_rope_create(self.desc)
+
+    def close(self):
+        if self.handle:
+            strata_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def apply(self, x, positions, out=None, stream=None):
+        """x [tokens, heads, head_dim] bf16 (any token and head strides), positions int32 [tokens]; out may be x."""
+        import torch
+        n, heads, D = x.shape
+        if out is None:
+            out = torch.empty((n, heads, D), dtype=x.dtype, device=x.device)
+        dev = x.device
+        _need(x, "x", torch.bfloat16)
+        _need(out, "out", torch.bfloat16, dev)
+        _need(positions, "positions", torch.int32, dev)
+        if D != self.head_dim or out.shape != x.shape or positions.shape != (n,):
+            raise ValueError(f"x {tuple(x.shape)}, out {tuple(out.shape)}, positions {tuple(positions.shape)}, "
+                             f"head_dim {self.head_dim}")
+        if x.stride(2) != 1 or out.stride(2) != 1 or not positions.is_contiguous():
+            raise ValueError("the values of a row and the positions must be contiguous")
+        with torch.cuda.device(dev):
+            strata_rope_apply(self.handle, x, x.stride(0), x.stride(1), positions, n, heads, out, out.stride(0),
+                              out.stride(1), stream)
+        return out
+
+
+class Kv4Cache:
+    """One layer's paged 4-bit KV cache over four tensors (kept alive): codes uint8 [pages, kv_heads, page_size,
+    head_dim / 2] and scales fp16 [pages, kv_heads, page_size, head_dim / 32], of keys and of values."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        import torch
+        pages, heads, page, half = k_codes.shape
+        self.device = k_codes.device
+        for name, t, dtype, last in (("k_codes", k_codes, torch.uint8, half), ("v_codes", v_codes, torch.uint8, half),
+                                     ("k_scales", k_scales, torch.float16, half // 16),
+                                     ("v_scales", v_scales, torch.float16, half // 16)):
+            _need(t, name, dtype, self.device)
+            if tuple(t.shape) != (pages, heads, page, last) or not t.is_contiguous():
+                raise ValueError(f"{name} {tuple(t.shape)} does not fit codes {tuple(k_codes.shape)}")
+        self.tensors = (k_codes, k_scales, v_codes, v_scales)
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, 2 * half
+        self.desc = strata_kv4_cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, heads, page,
+                                     2 * half)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_kv_heads, head_dim, device="cuda"):
+        """A cache of new, uninitialised pages."""
+        import torch
+        shape = (n_pages, n_kv_heads, page_size)
+        return cls(*(torch.empty((*shape, last), dtype=dtype, device=device)
+                     for last, dtype in 2 * ((head_dim // 2, torch.uint8), (head_dim // 32, torch.float16))))
+
+    def append(self, k, v, slots, rope=None, positions=None, stream=None):
+        """k, v [tokens, kv_heads, head_dim] bf16 (any token stride) into slots int64 [tokens] (page * page_size +
+        slot; negative: dropped), k through `rope` at positions int32 [tokens]."""
+        import torch
+        n = k.shape[0]
+        D, dev = self.head_dim, self.device
+        _need(k, "k", torch.bfloat16, dev)
+        _need(v, "v", torch.bfloat16, dev)
+        _need(slots, "slots", torch.int64, dev)
+        if tuple(k.shape) != (n, self.n_kv_heads, D) or v.shape != k.shape or tuple(slots.shape) != (n,):
+            raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)}, slots {tuple(slots.shape)}")
+        if n and (k.stride()[1:] != (D, 1) or v.stride()[1:] != (D, 1) or not slots.is_contiguous()):
+            raise ValueError("the heads of a token and the slots must be contiguous")
+        if rope is not None:
+            if positions is None:
+                raise ValueError("rope needs positions")
+            _need(positions, "positions", torch.int32, dev)
+            if tuple(positions.shape) != (n,) or not positions.is_contiguous():
+                raise ValueError(f"positions {tuple(positions.shape)}")
+        with torch.cuda.device(dev):
+            strata_kv4_append(self.desc, None if rope is None else rope.handle, k, k.stride(0), v, v.stride(0),
+                              positions if rope is not None else None, slots, n, stream)
+
+    def attention_workspace(self, n_q_heads):
+        """A workspace for attention() with n_q_heads query heads, whatever the sequences."""
+        import torch
+        n = strata_kv4_attention_workspace_bytes(self.desc, n_q_heads)
+        if n == 0:
+            raise ValueError(f"{n_q_heads} query heads over {self.n_kv_heads} KV heads")
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def attention(self, q, q_offsets, kv_lens, block_table, out=None, *, max_q_len, scale=None, window=0, rope=None,
+                  positions=None, workspace=None, stream=None):
+        """Causal attention of q [tokens, heads, head_dim] bf16 (any token stride). Sequence b: query rows
+        q_offsets[b] .. q_offsets[b + 1] - 1, the last of its kv_lens[b] cached tokens, on pages block_table[b]
+        (all int32); max_q_len its longest query run. Rows outside every sequence stay as they are in `out`."""
+        import torch
+        n, heads, D = q.shape
+        dev = self.device
+        if out is None:
+            out = torch.zeros((n, heads, D), dtype=q.dtype, device=dev)
+        _need(q, "q", torch.bfloat16, dev)
+        _need(out, "out", torch.bfloat16, dev)
+        for name, t in (("q_offsets", q_offsets), ("kv_lens", kv_lens), ("block_table", block_table)):
+            _need(t, name, torch.int32, dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        B = kv_lens.shape[0]
+        if D != self.head_dim or out.shape != q.shape or tuple(q_offsets.shape) != (B + 1,) or \
+                block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)}, q_offsets {tuple(q_offsets.shape)}, "
+                             f"kv_lens {tuple(kv_lens.shape)}, block_table {tuple(block_table.shape)}")
+        if n and (q.stride()[1:] != (D, 1) or out.stride()[1:] != (D, 1)):
+            raise ValueError("the heads of a token must be contiguous")
+        if rope is not None:
+            if positions is None:
+                raise ValueError("rope needs positions")
+            _need(positions, "positions", torch.int32, dev)
+            if tuple(positions.shape) != (n,) or not positions.is_contiguous():
+                raise ValueError(f"positions {tuple(positions.shape)}")
+        if workspace is None:
+            workspace = self.attention_workspace(heads)
+        desc = strata_kv4_attn_desc(B, heads, max_q_len, block_table.shape[1], n, q.stride(0), out.stride(0), window,
+                                    D ** -0.5 if scale is None else scale)
+        with torch.cuda.device(dev):
+            strata_kv4_attention(self.desc, desc, None if rope is None else rope.handle,
+                                 positions if rope is not None else None, q, q_offsets, kv_lens, block_table, out,
+                                 workspace, workspace.numel() * workspace.element_size(), stream)
+        return out
+
+
+class Kv4CacheSet:
+    """Several caches of one shape (a model's layers), whose pages are copied together."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if len({c.device for c in self.caches}) > 1:
+            raise ValueError("the caches of a set are on one device")
+        self.descs = (strata_kv4_cache * len(self.caches))(*(c.desc for c in self.caches))
+
+    def copy_pages(self, src, dst, stream=None):
+        """Page src[i] -> dst[i] in every cache; src and dst are host lists (see strata_kv4_copy_pages)."""
+        import torch
+        if self.caches:
+            with torch.cuda.device(self.caches[0].device):
+                strata_kv4_copy_pages(self.descs, src, dst, stream)

@@ -1,0 +1,135 @@
+// kv4_row.cuh -- device pieces shared by the kernels around the paged 4-bit
+// cache (include/strata_attn.h): the rotary table, the Walsh-Hadamard
+// transform of a row and the block rule of the codec (include/strata_kv.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/strata_attn.h"
+
+// Frequencies of a rotary handle, passed to kernels by value: freq[i] is
+// f_i / (2 pi) in turns per position, as a 64-bit fixed-point fraction.
+struct RopeTable {
+    uint64_t freq[STRATA_ROPE_MAX_HEAD_DIM / 2];
+    double m;    // factor of cosine and sine
+    int rd;      // rotary_dim; 0: no rotation
+    int half;    // 1: pairs (i, i + rd/2), 0: pairs (2i, 2i + 1)
+};
+
+struct strata_rope_s {
+    strata_rope_desc desc;
+    RopeTable table;
+};
+
+// Check a cache description; on failure the reason is the last error.
+strata_status strata_check_kv4_cache(const strata_kv4_cache *cache);
+
+namespace strata {
+
+constexpr unsigned kFullMask = 0xffffffffu;
+
+// position * f / (2 pi) modulo one turn: the product wraps modulo 2^64, which
+// is exactly one turn, so a far position loses no bits; as a signed fraction
+// of half turns in [-1, 1).
+__device__ __forceinline__ double half_turns(const RopeTable &t, int i, int position) {
+    return (double)(int64_t)((uint64_t)(int64_t)position * t.freq[i]) * 0x1p-63;
+}
+
+// (cos, sin) of pair i: fp64, rounded once to fp32 (the bits that
+// strata_rope_apply and strata_kv4_append promise)
+__device__ __forceinline__ float2 rope_cs(const RopeTable &t, int i, int position) {
+    double s, c;
+    sincospi(half_turns(t, i, position), &s, &c);
+    return make_float2((float)(c * t.m), (float)(s * t.m));
+}
+
+// the same in fp32, for a result that is not rounded to fixed bits: the exact
+// fraction of a turn, rounded to fp32, then two fp32 ulp of sincospif
+__device__ __forceinline__ float2 rope_cs_f32(const RopeTable &t, int i, int position) {
+    const float x = (float)(int64_t)((uint64_t)(int64_t)position * t.freq[i]) * 0x1p-63f;
+    float s, c;
+    sincospif(x, &s, &c);
+    return make_float2(c * (float)t.m, s * (float)t.m);
+}
+
+// u c - v s and v c + u s, each product and each sum rounded once
+__device__ __forceinline__ float rope_first(float u, float v, float2 cs) {
+    return __fsub_rn(__fmul_rn(u, cs.x), __fmul_rn(v, cs.y));
+}
+__device__ __forceinline__ float rope_second(float u, float v, float2 cs) {
+    return __fadd_rn(__fmul_rn(v, cs.x), __fmul_rn(u, cs.y));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Rotary partner of value i < rd of a row, and its pair
+__device__ __forceinline__ int rope_partner(const RopeTable &t, int i) {
+    return t.half ? (i < t.rd / 2 ? i + t.rd / 2 : i - t.rd / 2) : (i ^ 1);
+}
+__device__ __forceinline__ int rope_pair(const RopeTable &t, int i) {
+    return t.half ? (i < t.rd / 2 ? i : i - t.rd / 2) : (i >> 1);
+}
+__device__ __forceinline__ bool rope_is_second(const RopeTable &t, int i) {
+    return t.half ? i >= t.rd / 2 : (i & 1) != 0;
+}
+
+// fp32(1 / sqrt(D)), the transform's normalisation
+template <int D>
+__device__ __forceinline__ float rsqrt_dim() {
+    return D == 64 ? 0.125f : D == 128 ? 0.08838834764831844055f : 0.0625f;
+}
+
+// Unnormalised Walsh-Hadamard transform of a row held by a whole warp: lane l
+// has values l * (D/32) .. + D/32 - 1. Used where the rounding order is free.
+template <int D>
+__device__ __forceinline__ void fwht_warp(float (&v)[D / 32], int lane) {
+    constexpr int P = D / 32;
+#pragma unroll
+    for (int s = 1; s < P; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (!(i & s)) {
+                const float a = v[i], b = v[i + s];
+                v[i] = a + b;
+                v[i + s] = a - b;
+            }
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const float sg = (lane & s) ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = fmaf(sg, v[i], __shfl_xor_sync(kFullMask, v[i], s));
+    }
+}
+
+// One query row for the attention, held by a warp as fwht_warp lays it out:
+// bf16 load, rotary in fp32, H x / sqrt(D), times `scale`.
+template <int D>
+__device__ __forceinline__ void load_query_row(float (&v)[D / 32], const __nv_bfloat16 *x, const RopeTable &t,
+                                              int position, float scale, int lane) {
+    constexpr int P = D / 32;
+    const int i0 = lane * P;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        const int i = i0 + j;
+        float a = __bfloat162float(x[i]);
+        if (i < t.rd) {
+            const float b = __bfloat162float(x[rope_partner(t, i)]);
+            const float2 cs = rope_cs_f32(t, rope_pair(t, i), position);
+            a = rope_is_second(t, i) ? rope_second(b, a, cs) : rope_first(a, b, cs);
+        }
+        v[j] = a;
+    }
+    fwht_warp<D>(v, lane);
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] *= rsqrt_dim<D>() * scale;
+}
+
+}  // namespace strata
