@@ -5,9 +5,11 @@
 // for the stored row y = (c - 8) s, and sum_j p_j v'_j = H (sum_j p_j y_j) / sqrt D:
 // a query row is rotated once on the way in and its output once on the way
 // out, and the cache's rows are used as they are stored.
+#include <cfloat>
 #include <cmath>
 
 #include "abi_internal.h"
+#include "common.cuh"
 #include "kv4_row.cuh"
 
 using namespace strata;
@@ -21,64 +23,611 @@ struct AttnArgs {
     const __nv_bfloat16 *q;
     const int32_t *q_offsets, *kv_lens, *table;
     __nv_bfloat16 *out;
+    void *workspace;
     int group, page_shift;
     float scale_log2;  // scale * log2(e)
 };
 
-// One warp per (token, query head): every key in turn, running maximum and
-// sum of the softmax in registers.
+// Row r of a KV head's query rows (token-major, the group's heads inside), in
+// the rotated basis, doubled (see the scales' normalisation): back through
+// the transform, divided by its sum, rounded once.
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_rows(const __grid_constant__ RopeTable tab,
-                                                  const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32], float l, int64_t t0, int hk, int r,
+                                          int lane) {
     constexpr int P = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const int b = blockIdx.z;
-    if (h >= a.d.n_q_heads) return;
-    const int64_t n_tok = a.d.n_tokens;
-    const int64_t t0 = min(max((int64_t)a.q_offsets[b], (int64_t)0), n_tok);
-    const int64_t t1 = min(max((int64_t)a.q_offsets[b + 1], t0), n_tok);
-    const int L = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.d.max_pages << a.page_shift);
-    const int hk = h / a.group;
-    for (int64_t t = t0 + blockIdx.x; t < t1; t += gridDim.x) {
-        float q[P], o[P];
-        load_query_row<D>(q, a.q + t * a.d.q_token_stride + (int64_t)h * D, tab, tab.rd ? a.positions[t] : 0,
-                          a.scale_log2, lane);
+    const int i = r / a.group, h = hk * a.group + r - i * a.group;
+    const float f = l > 0.f ? 0.5f * rsqrt_dim<D>() / l : 0.f;
+    fwht_warp<D>(v, lane);
+    uint32_t w[P / 2];
 #pragma unroll
-        for (int i = 0; i < P; ++i) o[i] = 0.f;
-        const int64_t p = L - (t1 - t0) + (t - t0);
-        const int64_t lo = a.d.window > 0 ? max((int64_t)0, p - a.d.window + 1) : 0;
-        const int64_t hi = min((int64_t)L, p + 1);
-        float m = -INFINITY, l = 0.f;
-        for (int64_t j = lo; j < hi; ++j) {
-            const int page = a.table[(int64_t)b * a.d.max_pages + (j >> a.page_shift)];
-            if (page < 0 || page >= a.c.n_pages) continue;
-            const int64_t row = (((int64_t)page * a.c.n_kv_heads + hk) << a.page_shift) + (j & (a.c.page_size - 1));
-            const uint8_t *kc = static_cast<const uint8_t *>(a.c.k_codes) + row * (D / 2) + lane * (P / 2);
-            const uint8_t *vc = static_cast<const uint8_t *>(a.c.v_codes) + row * (D / 2) + lane * (P / 2);
-            const int64_t sc = row * (D / 32) + lane * P / 32;
-            const float ks = __half2float(static_cast<const __half *>(a.c.k_scales)[sc]);
-            const float vs = __half2float(static_cast<const __half *>(a.c.v_scales)[sc]);
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < P; ++i) s += q[i] * (float)((int)(kc[i / 2] >> (4 * (i & 1)) & 15) - 8);
-            s *= ks;
-#pragma unroll
-            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(kFullMask, s, x);
-            const float mn = fmaxf(m, s);
-            const float f = exp2f(m - mn), e = exp2f(s - mn);
-            l = l * f + e;
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                o[i] = o[i] * f + e * vs * (float)((int)(vc[i / 2] >> (4 * (i & 1)) & 15) - 8);
-            m = mn;
+    for (int j = 0; j < P / 2; ++j) w[j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
+    uint8_t *dst = reinterpret_cast<uint8_t *>(a.out + (t0 + i) * a.d.out_token_stride + (int64_t)h * D + lane * P);
+    if constexpr (P == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if constexpr (P == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    if constexpr (P == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------- few rows
+// k_attn_split: up to 8 NT query rows of a KV head (tokens x heads of the
+// group) against a long cache, which is read once. Bound by HBM, and close
+// behind by instruction issue: 18 D bytes and about 280 warp instructions a
+// 16-key tile, so everything around the matrix instructions is counted.
+//
+//   * S^T = K Q^T: keys are the 16 rows of m16n8k16, 8 query rows its columns.
+//     A code's nibble under the exponent of 1024 (or, at bits 4..7, of 64) is
+//     the exact fp16 value 1024 + c (64 + c); sum q (offset + 8) of a block is
+//     the same for every key and enters as the accumulator's start. A block's
+//     sum is scaled afterwards, in fp32: keys are never rounded.
+//   * O^T = V^T P^T: nibbles of two keys side by side, c - 8 exact in fp16;
+//     the probability takes the value's scale, p s. Both run in fp16, so a key
+//     j enters the running maximum with its value's exponent e_j: weights
+//     2^(x_j + e_j - M) <= 1 times s 2^(1 - e_j) in [2, 4), whatever the
+//     scales' magnitude, and the sum l takes 2^(x_j + e_j - M) 2^-e_j in fp32.
+//   * M moves only when a weight would pass 2^8: most tiles need no reduction
+//     over lanes.
+//
+// Work: the tiles of all (sequence, KV head, row group) in a row, cut into
+// equal runs of units, one for each CTA (one tile for each of the 8 warps), so that
+// any mix of lengths fills the machine. A run that covers a sequence's whole
+// cache writes its rows; the others leave (M, l, O) in the workspace, two at
+// most for a CTA, and k_attn_join adds them up in a fixed order.
+constexpr int kSms = 148;
+constexpr int kSplitParts = 2 * 16 * kSms;  // rows of partial results: 2 x 8 rows x 296 CTAs or 2 x 16 x 148
+constexpr int kSplitMaxCtas = 2 * kSms;
+constexpr int kSplitWarps = 8;
+constexpr int kStages = 4;
+constexpr int kTile = 16;        // keys: no tile crosses a page
+
+struct Span {  // what k_attn_join needs of the last piece of a CTA
+    int parts;  // CTAs that share it, 0: none
+    int slot;   // of the first one; 0 for the others
+    int t0, rows, hk, row0;
+    int pad[2];
+};
+
+template <int D, int NT>
+struct Split {
+    static constexpr int NB = D / 32;
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int STAGE = 18 * D;             // codes 16 D, scales 2 D
+    static constexpr int RING = kStages * STAGE;     // of a warp; holds its rows of O at a piece's end
+    static constexpr int OROW = D + 4;
+    static constexpr int SCRATCH = D + 16 * 8;       // scaled V scales of a tile, (e, 2^-e) of its keys
+    static constexpr int PART = D + 4;               // floats of a part in the workspace: O, M, l
+    static constexpr int SMEM = kSplitWarps * (RING + SCRATCH) + ROWS * D * 2 + ROWS * NB * 4 + ROWS * 4 +
+                                2 * kSplitWarps * ROWS * 4;
+    static_assert(ROWS * OROW * 4 <= RING, "O of a warp fits its ring");
+    static constexpr int CTAS_PER_SM = NT == 1 && D <= 128 ? 2 : 1;
+    static constexpr int CTAS = kSms * CTAS_PER_SM;
+    static_assert(2 * ROWS * CTAS <= kSplitParts && CTAS <= kSplitMaxCtas, "workspace");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// (w & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+
+// 16-byte chunk c of row r of a code tile: shifted so that both readers, 8
+// rows at one chunk and every second row at one chunk, meet 32 banks
+template <int D>
+__device__ __forceinline__ int code_chunk(int r, int c) {
+    constexpr int NB = D / 32;
+    const int x = D == 64 ? (r >> 2) & 1 : D == 128 ? (r >> 1) & 3 : r & 7;
+    return r * (D / 2) + ((c ^ x) & (NB - 1)) * 16;
+}
+
+struct Seq {  // one sequence as the kernels see it
+    int64_t t0;
+    int n, L, tile0, tiles, groups;
+};
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_group) {
+    Seq s;
+    s.t0 = min(max((int64_t)a.q_offsets[b], (int64_t)0), a.d.n_tokens);
+    s.n = (int)(min(max((int64_t)a.q_offsets[b + 1], s.t0), a.d.n_tokens) - s.t0);
+    s.L = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.d.max_pages << a.page_shift);
+    const int64_t first = a.d.window > 0 ? max((int64_t)0, (int64_t)s.L - s.n - a.d.window + 1) : 0;
+    s.tile0 = (int)(min(first, (int64_t)s.L) / kTile);
+    s.tiles = (int)(((int64_t)s.L + kTile - 1) / kTile) - s.tile0;
+    s.groups = (int)(((int64_t)s.n * a.group + rows_per_group - 1) / rows_per_group);
+    return s;
+}
+// units of one (KV head, row group); one at least, which writes the zeros of a
+// sequence without keys
+__device__ __forceinline__ int64_t seq_units(const Seq &s) { return max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
+
+// total * i / n, rounded down: where run i of n starts
+__device__ __forceinline__ int64_t run_start(int64_t total, int64_t i, int64_t n) {
+    return (int64_t)((uint64_t)total * (uint64_t)i / (uint64_t)n);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
+    k_attn_split(const __grid_constant__ RopeTable tab, const __grid_constant__ AttnArgs a) {
+    using C = Split<D, NT>;
+    constexpr int NB = C::NB, ROWS = C::ROWS, P = D / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t *ring = smem + warp * C::RING;
+    uint8_t *scratch = smem + kSplitWarps * C::RING + warp * C::SCRATCH;
+    __half *sq = reinterpret_cast<__half *>(smem + kSplitWarps * (C::RING + C::SCRATCH));
+    float *scorr = reinterpret_cast<float *>(sq + ROWS * D);
+    float *sfac = scorr + ROWS * NB;
+    float *sM = sfac + ROWS, *sl = sM + kSplitWarps * ROWS;
+    __shared__ int64_t s_sum[kSplitWarps];
+    __shared__ int64_t s_total, s_before;
+    __shared__ int s_b;
+    griddep_launch_dependents();
+
+    // ---- this CTA's run of units, and the sequence it starts in
+    int64_t total = 0, u_lo = 0, u_hi = 0;
+    int ctas = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass) {
+            ctas = (int)min(total, (int64_t)C::CTAS);  // a unit each at least
+            if (blockIdx.x >= ctas) break;
+            u_lo = run_start(total, blockIdx.x, ctas);
+            u_hi = run_start(total, blockIdx.x + 1, ctas);
         }
-        const float r = l > 0.f ? rsqrt_dim<D>() / l : 0.f;
-        fwht_warp<D>(o, lane);
+        int64_t run = 0;
+        for (int b0 = 0; b0 < a.d.n_seqs; b0 += kSplitWarps * 32) {
+            const int b = b0 + threadIdx.x;
+            int64_t v = 0;
+            if (b < a.d.n_seqs) {
+                const Seq s = seq_of(a, b, ROWS);
+                v = seq_units(s) * s.groups * a.c.n_kv_heads;
+            }
+            int64_t inc = v;
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            a.out[t * a.d.out_token_stride + (int64_t)h * D + lane * P + i] = __float2bfloat16_rn(o[i] * r);
+            for (int x = 1; x < 32; x <<= 1) {
+                const int64_t o = __shfl_up_sync(kFullMask, inc, x);
+                if (lane >= x) inc += o;
+            }
+            if (lane == 31) s_sum[warp] = inc;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) inc += s_sum[w];
+            inc += run;
+            if (threadIdx.x == kSplitWarps * 32 - 1) s_total = inc;
+            if (pass && inc - v <= u_lo && u_lo < inc) {
+                s_b = b;
+                s_before = inc - v;
+            }
+            __syncthreads();
+            run = s_total;
+            if (pass && run > u_lo) break;
+        }
+        if (!pass) total = run;
     }
+    Span *spans = static_cast<Span *>(a.workspace);
+    float *parts = reinterpret_cast<float *>(spans + kSplitMaxCtas);
+    if (u_lo == u_hi) {
+        if (threadIdx.x == 0) spans[blockIdx.x].parts = 0;
+        return;
+    }
+    int b = s_b;
+    Seq s = seq_of(a, b, ROWS);
+    int64_t per = seq_units(s);
+    int64_t vh = (u_lo - s_before) / per;        // (KV head, row group) inside the sequence
+    int64_t first = s_before + vh * per;         // its first unit
+    int span_parts = 0, span_slot = 0, span_hk = 0, span_row0 = 0, span_t0 = 0, span_rows = 0;
+
+    for (int64_t u = u_lo; u < u_hi;) {
+        const int64_t u_end = min(first + per, u_hi);
+        const int rg = (int)(vh / a.c.n_kv_heads), hk = (int)(vh - (int64_t)rg * a.c.n_kv_heads);
+        const int row0 = rg * ROWS;
+        const int rows = min(ROWS, s.n * a.group - row0);
+        const int p_first = s.L - s.n;           // position of query 0
+
+        // ---- the warp's tiles: tile0 + 8 unit + warp
+        int it = s.tile0 + (int)(u - first) * kSplitWarps + warp;
+        const int t_end = min(s.tile0 + s.tiles, s.tile0 + (int)(u_end - first) * kSplitWarps);
+        const int32_t *table = a.table + (int64_t)b * a.d.max_pages;
+        const int tile_shift = a.page_shift - 4;
+        int nit = it, page = -1;                 // next tile to ask for, and its page
+        uint32_t there = 0;                      // bit s: stage s holds a tile
+        if (nit < t_end) page = __ldg(table + (nit >> tile_shift));
+        auto issue = [&](int stage) {
+            const bool ok = nit < t_end && page >= 0 && page < a.c.n_pages;
+            there = (there & ~(1u << stage)) | ((ok ? 1u : 0u) << stage);
+            if (ok) {
+                const int64_t row = (((int64_t)page * a.c.n_kv_heads + hk) << a.page_shift) +
+                                    ((nit & ((1 << tile_shift) - 1)) << 4);
+                uint8_t *st = ring + stage * C::STAGE;
+                const uint8_t *kc = static_cast<const uint8_t *>(a.c.k_codes) + row * (D / 2);
+                const uint8_t *vc = static_cast<const uint8_t *>(a.c.v_codes) + row * (D / 2);
+#pragma unroll
+                for (int i = 0; i < (16 * NB + 31) / 32; ++i) {
+                    const int c = lane + 32 * i, r = c / NB, ch = c % NB;
+                    cp_async16(st + code_chunk<D>(r, ch), kc + c * 16);
+                    cp_async16(st + 8 * D + code_chunk<D>(r, ch), vc + c * 16);
+                }
+                if (lane < 4 * NB) {             // scales: 2 NB chunks of keys, then of values
+                    const int c = lane < 2 * NB ? lane : lane - 2 * NB;
+                    const uint8_t *sc = static_cast<const uint8_t *>(lane < 2 * NB ? a.c.k_scales : a.c.v_scales);
+                    cp_async16(st + 16 * D + lane * 16, sc + row * (D / 16) + c * 16);
+                }
+            }
+            cp_async_commit();
+            nit += kSplitWarps;
+            if (nit < t_end) page = __ldg(table + (nit >> tile_shift));
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+        // ---- query rows: rotary, transform, fp16 with a power-of-two scale
+        for (int r = warp; r < ROWS; r += kSplitWarps) {
+            float v[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = 0.f;
+            if (r < rows) {
+                const int i = (row0 + r) / a.group, h = hk * a.group + (row0 + r) - i * a.group;
+                const int64_t tok = s.t0 + i;
+                load_query_row<D>(v, a.q + tok * a.d.q_token_stride + (int64_t)h * D, tab,
+                                  tab.rd ? a.positions[tok] : 0, 1.f, lane);
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
+            const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 253u);
+            const float mul = m > 0.f ? __uint_as_float((254u - ex) << 23) : 1.f;  // largest value to [1, 2)
+            float corr = 0.f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int d = lane * P + i, n = d & 7;
+                const __half q = __float2half_rn(v[i] * mul);
+                sq[r * D + (d & ~7) + (n < 4 ? 2 * n : 2 * n - 7)] = q;
+                corr = fmaf(__half2float(q), (d & 1) ? -72.f : -1032.f, corr);
+            }
+#pragma unroll
+            for (int x = 1; x < 32 / NB; x <<= 1) corr += __shfl_xor_sync(kFullMask, corr, x);
+            if ((lane & (32 / NB - 1)) == 0) scorr[r * NB + lane / (32 / NB)] = corr;
+            if (lane == 0) sfac[r] = a.scale_log2 * (m > 0.f ? __uint_as_float(ex << 23) : 1.f);
+        }
+        __syncthreads();
+        uint32_t qf[NT][NB][4];
+        float corr[NT][NB][2], fac[NT][2], M[NT][2], l[NT][2], o[NT][2 * NB][4];
+        int hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(sq + (n * 8 + g) * D + 32 * k + 8 * t);
+                qf[n][k][0] = w.x, qf[n][k][1] = w.y, qf[n][k][2] = w.z, qf[n][k][3] = w.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = n * 8 + 2 * t + j;
+#pragma unroll
+                for (int k = 0; k < NB; ++k) corr[n][k][j] = scorr[r * NB + k];
+                fac[n][j] = sfac[r];
+                const int p = p_first + (row0 + r) / a.group;
+                hi[n][j] = min(p, s.L - 1);
+                lo[n][j] = a.d.window > 0 ? (int)max((int64_t)p - a.d.window, (int64_t)-1) : -1;
+                M[n][j] = -FLT_MAX;
+                l[n][j] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
+        }
+        // tiles up to here, and from there on, need no mask
+        const int last_row = (row0 + rows - 1) / a.group;
+        const int full_hi = p_first + row0 / a.group;
+        const int full_lo = a.d.window > 0 ? (int)max((int64_t)p_first + last_row - a.d.window, (int64_t)-1) : -1;
+
+        uint32_t *vs = reinterpret_cast<uint32_t *>(scratch);         // [8 key pairs][NB] half2
+        float2 *ve = reinterpret_cast<float2 *>(scratch + D);         // [16 keys] (e, 2^-e)
+        for (int stage = 0; it < t_end; it += kSplitWarps, stage = (stage + 1) & (kStages - 1)) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            issue((stage + kStages - 1) & (kStages - 1));
+            if (!(there >> stage & 1)) continue;
+            const uint8_t *st = ring + stage * C::STAGE;
+            const int j0 = it * kTile;
+
+            // V scales: normalised per key, in key pairs
+            {
+                const __half *sc = reinterpret_cast<const __half *>(st + 17 * D);
+                const bool in0 = j0 + 2 * g < s.L, in1 = j0 + 2 * g + 1 < s.L;
+                __half2 x[(NB + 3) / 4], m = __float2half2_rn(0.f);
+#pragma unroll
+                for (int i = 0; i < (NB + 3) / 4; ++i) {
+                    const int k = (t + 4 * i) & (NB - 1);
+                    x[i] = __halves2half2(in0 ? sc[2 * g * NB + k] : __half(0.f), in1 ? sc[(2 * g + 1) * NB + k] : __half(0.f));
+                    m = __hmax2(m, __habs2(x[i]));
+                }
+                m = __hmax2(m, bits_h2(__shfl_xor_sync(kFullMask, h2_bits(m), 1)));
+                m = __hmax2(m, bits_h2(__shfl_xor_sync(kFullMask, h2_bits(m), 2)));
+                const uint32_t e = __vmaxu2(h2_bits(m) & 0x7c007c00u, 0x04000400u);
+                const __half2 mul = bits_h2(0x7c007c00u - e);          // 2^(1 - e)
+#pragma unroll
+                for (int i = 0; i < (NB + 3) / 4; ++i)
+                    if (t + 4 * i < NB) vs[g * NB + t + 4 * i] = h2_bits(__hmul2(x[i], mul));
+                if (t == 0) {
+                    const int e0 = (int)(e >> 10 & 31) - 15, e1 = (int)(e >> 26) - 15;
+                    *reinterpret_cast<float4 *>(ve + 2 * g) =
+                        make_float4((float)e0, __int_as_float((127 - e0) << 23), (float)e1, __int_as_float((127 - e1) << 23));
+                }
+            }
+            // S^T
+            float x[NT][4];
+            {
+                float ks[2][NB];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const __half2 *sc = reinterpret_cast<const __half2 *>(st + 16 * D + (g + 8 * r) * NB * 2);
+                    uint32_t w[NB / 2];
+                    if constexpr (NB == 2) w[0] = *reinterpret_cast<const uint32_t *>(sc);
+                    if constexpr (NB == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(sc);
+                    if constexpr (NB == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(sc);
+#pragma unroll
+                    for (int k = 0; k < NB / 2; ++k) {
+                        const float2 f = __half22float2(bits_h2(w[k]));
+                        ks[r][2 * k] = f.x, ks[r][2 * k + 1] = f.y;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(st + code_chunk<D>(g, k) + 4 * t);
+                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(st + code_chunk<D>(g + 8, k) + 4 * t);
+                    const uint32_t a0[4] = {and_or(w0, 0x000f000fu, 0x64006400u), and_or(w1, 0x000f000fu, 0x64006400u),
+                                            and_or(w0, 0x00f000f0u, 0x54005400u), and_or(w1, 0x00f000f0u, 0x54005400u)};
+                    const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+                    const uint32_t a1[4] = {and_or(h0, 0x000f000fu, 0x64006400u), and_or(h1, 0x000f000fu, 0x64006400u),
+                                            and_or(h0, 0x00f000f0u, 0x54005400u), and_or(h1, 0x00f000f0u, 0x54005400u)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float c[4];
+                        const float c0[4] = {corr[n][k][0], corr[n][k][1], corr[n][k][0], corr[n][k][1]};
+                        mma16816(c, a0, qf[n][k][0], qf[n][k][1], c0);
+                        mma16816(c, a1, qf[n][k][2], qf[n][k][3], c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[n][j] = k ? fmaf(c[j], ks[j >> 1][k], x[n][j]) : c[j] * ks[j >> 1][k];
+                    }
+                }
+            }
+            __syncwarp();
+            // softmax: weights of keys g, g + 8 for query rows 2t, 2t + 1
+            const float2 e0 = ve[g], e1 = ve[g + 8];
+            const bool whole = j0 + kTile - 1 <= full_hi && j0 > full_lo;
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[n][j] = fmaf(x[n][j], fac[n][j & 1], j < 2 ? e0.x : e1.x);
+                    if (!whole) {
+                        const int pos = j0 + g + (j < 2 ? 0 : 8);
+                        if (pos > hi[n][j & 1] || pos <= lo[n][j & 1]) x[n][j] = -INFINITY;
+                    }
+                }
+                grow |= fmaxf(x[n][0], x[n][2]) > M[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) > M[n][1] + 8.f;
+            }
+            if (__any_sync(kFullMask, grow)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float m = fmaxf(M[n][j], fmaxf(x[n][j], x[n][j + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
+                        const float f = ex2(M[n][j] - m);
+                        M[n][j] = m;
+                        l[n][j] *= f;
+#pragma unroll
+                        for (int k = 0; k < 2 * NB; ++k) o[n][k][j] *= f, o[n][k][j + 2] *= f;
+                    }
+            }
+            uint32_t p0[NT], p1[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[n][j] = ex2(x[n][j] - M[n][j & 1]);
+                    l[n][j & 1] = fmaf(x[n][j], j < 2 ? e0.y : e1.y, l[n][j & 1]);
+                }
+                p0[n] = transpose8x8(h2_bits(__floats2half2_rn(x[n][0], x[n][1])));  // keys 2t, 2t + 1
+                p1[n] = transpose8x8(h2_bits(__floats2half2_rn(x[n][2], x[n][3])));  // keys 2t + 8, 2t + 9
+            }
+            // O^T
+            const uint8_t *vt = st + 8 * D + 4 * (g >> 1);
+            const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // values 4g .. 4g + 3 of a block
+            const __half2 off = __floats2half2_rn(-1032.f, -1032.f), off64 = __floats2half2_rn(-72.f, -72.f);
+            auto unpack = [&](uint32_t w, uint32_t (&v)[4]) {
+                const uint32_t h = w >> 8;
+                v[0] = h2_bits(__hadd2(bits_h2(and_or(w, 0x000f000fu, 0x64006400u)), off));
+                v[1] = h2_bits(__hadd2(bits_h2(and_or(w, 0x00f000f0u, 0x54005400u)), off64));
+                v[2] = h2_bits(__hadd2(bits_h2(and_or(h, 0x000f000fu, 0x64006400u)), off));
+                v[3] = h2_bits(__hadd2(bits_h2(and_or(h, 0x00f000f0u, 0x54005400u)), off64));
+            };
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = *reinterpret_cast<const uint32_t *>(vt + code_chunk<D>(2 * t + (j & 1) + (j >> 1) * 8, k));
+                uint32_t v0[4], v1[4];
+                unpack(__byte_perm(w[0], w[1], sel), v0);
+                unpack(__byte_perm(w[2], w[3], sel), v1);
+                const __half2 s0 = bits_h2(vs[t * NB + k]), s1 = bits_h2(vs[(t + 4) * NB + k]);
+                const uint32_t a0[4] = {v0[0], v0[1], v1[0], v1[1]}, a1[4] = {v0[2], v0[3], v1[2], v1[3]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t b0 = h2_bits(__hmul2(bits_h2(p0[n]), s0)), b1 = h2_bits(__hmul2(bits_h2(p1[n]), s1));
+                    mma16816(o[n][2 * k], a0, b0, b1, o[n][2 * k]);
+                    mma16816(o[n][2 * k + 1], a1, b0, b1, o[n][2 * k + 1]);
+                }
+            }
+            __syncwarp();  // the scratch and the stage are written again
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+
+        // ---- join the 8 warps
+        float *so = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = n * 8 + 2 * t + j;
+                float sum = l[n][j];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+                if (g == 0) {
+                    sM[warp * ROWS + r] = M[n][j];
+                    sl[warp * ROWS + r] = sum;
+                }
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+                    *reinterpret_cast<float4 *>(so + r * C::OROW + 32 * k + 4 * g) =
+                        make_float4(o[n][2 * k][j], o[n][2 * k][j + 2], o[n][2 * k + 1][j], o[n][2 * k + 1][j + 2]);
+            }
+        __syncthreads();
+        const bool whole = u == first && u_end == first + per;
+        const int slot = u == u_lo ? 0 : 1;
+        for (int r = warp; r < rows; r += kSplitWarps) {
+            float m = sM[r];
+#pragma unroll
+            for (int w = 1; w < kSplitWarps; ++w) m = fmaxf(m, sM[w * ROWS + r]);
+            float sum = 0.f, v[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kSplitWarps; ++w) {
+                const float f = ex2(sM[w * ROWS + r] - m);
+                sum = fmaf(sl[w * ROWS + r], f, sum);
+                const float *ow = reinterpret_cast<const float *>(smem + w * C::RING) + r * C::OROW + lane * P;
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[i] = fmaf(ow[i], f, v[i]);
+            }
+            if (whole) {
+                store_row<D>(a, v, sum, s.t0, hk, row0 + r, lane);
+            } else {
+                float *part = parts + (int64_t)((blockIdx.x * 2 + slot) * ROWS + r) * C::PART;
+#pragma unroll
+                for (int i = 0; i < P; ++i) part[lane * P + i] = v[i];
+                if (lane == 0) part[D] = m, part[D + 1] = sum;
+            }
+        }
+        if (u == first && u_end < first + per) {
+            // it starts here and ends in the CTA that holds its last unit
+            const int64_t last = first + per - 1;
+            int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
+            while (run_start(total, c + 1, ctas) <= last) ++c;
+            span_parts = c - blockIdx.x + 1;
+            span_slot = slot, span_hk = hk, span_row0 = row0, span_t0 = (int)s.t0, span_rows = rows;
+        }
+        __syncthreads();
+        u = u_end;
+        if (u < u_hi) {
+            first += per;
+            if (++vh == (int64_t)s.groups * a.c.n_kv_heads) {
+                vh = 0;
+                do {
+                    s = seq_of(a, ++b, ROWS);
+                } while (s.groups == 0);
+                per = seq_units(s);
+            }
+        }
+    }
+    if (threadIdx.x == 0) spans[blockIdx.x] = Span{span_parts, span_slot, span_t0, span_rows, span_hk, span_row0, {0, 0}};
+}
+
+// One block for each query row of a piece that several CTAs share: 8 warps
+// over its parts, then over each other, in a fixed order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a) {
+    constexpr int P = D / 32, PART = D + 4;
+    __shared__ float so[8][D], sl[8], sm[8];
+    griddep_wait();
+    const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
+    const int r = blockIdx.y;
+    if (sp.parts == 0 || r >= sp.rows) return;
+    const float *parts = reinterpret_cast<const float *>(static_cast<const Span *>(a.workspace) + kSplitMaxCtas);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto at = [&](int i) {
+        return parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
+    };
+    float m = -FLT_MAX;
+    for (int i = threadIdx.x; i < sp.parts; i += 256) m = fmaxf(m, at(i)[D]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
+    if (lane == 0) sm[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, sm[w]);
+    float v[P], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] = 0.f;
+    for (int i = warp; i < sp.parts; i += 8) {
+        const float *p = at(i);
+        const float f = ex2(p[D] - m);
+        sum = fmaf(p[D + 1], f, sum);
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] = fmaf(p[lane * P + j], f, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < P; ++j) so[warp][lane * P + j] = v[j];
+    if (lane == 0) sl[warp] = sum;
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+        sum += sl[w];
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] += so[w][lane * P + j];
+    }
+    store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
+}
+
+template <int D, int NT>
+cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
+    using C = Split<D, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    k_attn_split<D, NT><<<C::CTAS, kSplitWarps * 32, C::SMEM, st>>>(tab, a);
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C::CTAS, C::ROWS);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_join<D, C::ROWS>, a);
 }
 
 }  // namespace
@@ -86,7 +635,7 @@ __global__ void __launch_bounds__(128) k_attn_rows(const __grid_constant__ RopeT
 extern "C" size_t strata_kv4_attention_workspace_bytes(const strata_kv4_cache *cache, int32_t n_q_heads) {
     if (strata_check_kv4_cache(cache) != STRATA_OK) return 0;
     if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return 0;
-    return 16;
+    return sizeof(Span) * kSplitMaxCtas + sizeof(float) * (cache->head_dim + 4) * kSplitParts;
 }
 
 extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, const strata_kv4_attn_desc *d,
@@ -127,19 +676,18 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
     static const RopeTable none = {};
     const RopeTable &tab = rope ? rope->table : none;
     AttnArgs a{*cache, *d, positions, static_cast<const __nv_bfloat16 *>(q), q_offsets, kv_lens, block_table,
-               static_cast<__nv_bfloat16 *>(out), d->n_q_heads / cache->n_kv_heads, 0, 0.f};
+               static_cast<__nv_bfloat16 *>(out), workspace, d->n_q_heads / cache->n_kv_heads, 0, 0.f};
     while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
     a.scale_log2 = d->scale * 1.44269504088896340736f;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int gx = d->max_q_len < 1 ? 1 : d->max_q_len < 65536 ? d->max_q_len : 65536;
-    const dim3 grid(gx, (d->n_q_heads + 3) / 4, d->n_seqs);
+    const bool two = (int64_t)d->max_q_len * a.group > 8;
+    cudaError_t e;
     if (cache->head_dim == 64)
-        k_attn_rows<64><<<grid, 128, 0, st>>>(tab, a);
+        e = two ? launch_split<64, 2>(tab, a, st) : launch_split<64, 1>(tab, a, st);
     else if (cache->head_dim == 128)
-        k_attn_rows<128><<<grid, 128, 0, st>>>(tab, a);
+        e = two ? launch_split<128, 2>(tab, a, st) : launch_split<128, 1>(tab, a, st);
     else
-        k_attn_rows<256><<<grid, 128, 0, st>>>(tab, a);
-    const cudaError_t e = cudaGetLastError();
+        e = launch_split<256, 1>(tab, a, st);
     if (e != cudaSuccess) return strata_set_error(STRATA_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return STRATA_OK;
 }
