@@ -29,14 +29,14 @@ struct AttnArgs {
 };
 
 // Row r of a KV head's query rows (token-major, the group's heads inside), in
-// the rotated basis, doubled (see the scales' normalisation): back through
-// the transform, divided by its sum, rounded once.
+// the rotated basis: back through the transform, divided by its sum, rounded
+// once.
 template <int D>
 __device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32], float l, int64_t t0, int hk, int r,
                                           int lane) {
     constexpr int P = D / 32;
     const int i = r / a.group, h = hk * a.group + r - i * a.group;
-    const float f = l > 0.f ? 0.5f * rsqrt_dim<D>() / l : 0.f;
+    const float f = l > 0.f ? rsqrt_dim<D>() / l : 0.f;
     fwht_warp<D>(v, lane);
     uint32_t w[P / 2];
 #pragma unroll
@@ -55,15 +55,17 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32],
 //
 //   * S^T = K Q^T: keys are the 16 rows of m16n8k16, 8 query rows its columns.
 //     A code's nibble under the exponent of 1024 (or, at bits 4..7, of 64) is
-//     the exact fp16 value 1024 + c (64 + c); sum q (offset + 8) of a block is
-//     the same for every key and enters as the accumulator's start. A block's
-//     sum is scaled afterwards, in fp32: keys are never rounded.
+//     the exact fp16 value 1024 + c (64 + c). A block's sum is scaled in fp32,
+//     so keys are never rounded; the offsets' share, -sum_b s_b sum_i q_i
+//     (offset + 8), is one product more, of the scales with the query's block
+//     sums (fp16 in two parts).
 //   * O^T = V^T P^T: nibbles of two keys side by side, c - 8 exact in fp16;
-//     the probability takes the value's scale, p s. Both run in fp16, so a key
-//     j enters the running maximum with its value's exponent e_j: weights
-//     2^(x_j + e_j - M) <= 1 times s 2^(1 - e_j) in [2, 4), whatever the
-//     scales' magnitude, and the sum l takes 2^(x_j + e_j - M) 2^-e_j in fp32.
-//   * M moves only when a weight would pass 2^8: most tiles need no reduction
+//     the probability takes the value's scale, p s, in fp16. Weights are
+//     2^(x - M + 6), so that a long tail under one large weight stays among
+//     fp16's normal numbers. Where a tile's scales are not all below 2^4 with
+//     some above 2^-6, a key enters with its own exponent e of them: 2^(x + e -
+//     M + 6) times s 2^(1 - e) in [2, 4), and the sum l takes the weight by 2^-e.
+//   * M moves only when a weight would pass 2^11: most tiles need no reduction
 //     over lanes.
 //
 // Work: the tiles of all (sequence, KV head, row group) in a row, cut into
@@ -75,8 +77,8 @@ constexpr int kSms = 148;
 constexpr int kSplitParts = 2 * 16 * kSms;  // rows of partial results: 2 x 8 rows x 296 CTAs or 2 x 16 x 148
 constexpr int kSplitMaxCtas = 2 * kSms;
 constexpr int kSplitWarps = 8;
-constexpr int kStages = 4;
-constexpr int kTile = 16;        // keys: no tile crosses a page
+constexpr int kStages = 2;  // a warp's own work on a tile covers the latency of the next
+constexpr int kTile = 32;   // keys, as two halves of 16: no half crosses a page
 
 struct Span {  // what k_attn_join needs of the last piece of a CTA
     int parts;  // CTAs that share it, 0: none
@@ -89,13 +91,13 @@ template <int D, int NT>
 struct Split {
     static constexpr int NB = D / 32;
     static constexpr int ROWS = 8 * NT;
-    static constexpr int STAGE = 18 * D;             // codes 16 D, scales 2 D
+    static constexpr int STAGE = 36 * D;             // codes 32 D, scales 4 D
     static constexpr int RING = kStages * STAGE;     // of a warp; holds its rows of O at a piece's end
     static constexpr int OROW = D + 4;
-    static constexpr int SCRATCH = D + 16 * 8;       // scaled V scales of a tile, (e, 2^-e) of its keys
+    static constexpr int SCRATCH = 2 * D + 32 * 8;   // scaled V scales of a tile, (e, 2^-e) of its keys
     static constexpr int PART = D + 4;               // floats of a part in the workspace: O, M, l
-    static constexpr int SMEM = kSplitWarps * (RING + SCRATCH) + ROWS * D * 2 + ROWS * NB * 4 + ROWS * 4 +
-                                2 * kSplitWarps * ROWS * 4;
+    static constexpr int SMEM = kSplitWarps * (RING + SCRATCH) + ROWS * D * 2 + ROWS * NB * 4 * 2 + ROWS * 4 +
+                                2 * kSplitWarps * ROWS * 4 + 128;
     static_assert(ROWS * OROW * 4 <= RING, "O of a warp fits its ring");
     static constexpr int CTAS_PER_SM = NT == 1 && D <= 128 ? 2 : 1;
     static constexpr int CTAS = kSms * CTAS_PER_SM;
@@ -107,8 +109,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -136,6 +138,32 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 
+template <int OFF = 0>
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(addr), "n"(OFF) : "memory");
+    return v;
+}
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
+    if constexpr (W == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    if constexpr (W == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    if constexpr (W >= 4)
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(addr + 4 * i) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_half(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // 16-byte chunk c of row r of a code tile: shifted so that both readers, 8
 // rows at one chunk and every second row at one chunk, meet 32 banks
 template <int D>
@@ -144,6 +172,12 @@ __device__ __forceinline__ int code_chunk(int r, int c) {
     const int x = D == 64 ? (r >> 2) & 1 : D == 128 ? (r >> 1) & 3 : r & 7;
     return r * (D / 2) + ((c ^ x) & (NB - 1)) * 16;
 }
+// Within 16-key tiles x(r + 8) = x(r), and for even r x(r + 1) = x(r) (^ 1 for
+// D = 256): a lane needs one address, one XOR for each block.
+
+// A value that is the same in every lane, so that the compiler sees it is:
+// branches on it need no reconvergence
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFullMask, v, 0); }
 
 struct Seq {  // one sequence as the kernels see it
     int64_t t0;
@@ -162,7 +196,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_gro
 }
 // units of one (KV head, row group); one at least, which writes the zeros of a
 // sequence without keys
-__device__ __forceinline__ int64_t seq_units(const Seq &s) { return max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
+__device__ __forceinline__ int seq_units(const Seq &s) { return max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
 
 // total * i / n, rounded down: where run i of n starts
 __device__ __forceinline__ int64_t run_start(int64_t total, int64_t i, int64_t n) {
@@ -174,111 +208,139 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
     k_attn_split(const __grid_constant__ RopeTable tab, const __grid_constant__ AttnArgs a) {
     using C = Split<D, NT>;
     constexpr int NB = C::NB, ROWS = C::ROWS, P = D / 32;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     uint8_t *ring = smem + warp * C::RING;
     uint8_t *scratch = smem + kSplitWarps * C::RING + warp * C::SCRATCH;
     __half *sq = reinterpret_cast<__half *>(smem + kSplitWarps * (C::RING + C::SCRATCH));
-    float *scorr = reinterpret_cast<float *>(sq + ROWS * D);
-    float *sfac = scorr + ROWS * NB;
+    __half *scorr = sq + ROWS * D;  // [ROWS][2][NB]: the two parts of a block's offset sum
+    float *sfac = reinterpret_cast<float *>(scorr + ROWS * NB * 4);
     float *sM = sfac + ROWS, *sl = sM + kSplitWarps * ROWS;
     __shared__ int64_t s_sum[kSplitWarps];
-    __shared__ int64_t s_total, s_before;
+    __shared__ int64_t s_before;
     __shared__ int s_b;
     griddep_launch_dependents();
 
     // ---- this CTA's run of units, and the sequence it starts in
-    int64_t total = 0, u_lo = 0, u_hi = 0;
+    int64_t total = 0, u_lo = 0, u_hi = 0, run = 0, inc = 0, v = 0;
     int ctas = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        if (pass) {
-            ctas = (int)min(total, (int64_t)C::CTAS);  // a unit each at least
-            if (blockIdx.x >= ctas) break;
-            u_lo = run_start(total, blockIdx.x, ctas);
-            u_hi = run_start(total, blockIdx.x + 1, ctas);
+    constexpr int kChunk = kSplitWarps * 32;
+    auto scan = [&](int b0) {  // inc: units up to and with sequence b0 + threadIdx.x; run: with the whole chunk
+        const int b = b0 + threadIdx.x;
+        v = 0;
+        if (b < a.d.n_seqs) {
+            const Seq s = seq_of(a, b, ROWS);
+            v = (int64_t)seq_units(s) * s.groups * a.c.n_kv_heads;
         }
-        int64_t run = 0;
-        for (int b0 = 0; b0 < a.d.n_seqs; b0 += kSplitWarps * 32) {
-            const int b = b0 + threadIdx.x;
-            int64_t v = 0;
-            if (b < a.d.n_seqs) {
-                const Seq s = seq_of(a, b, ROWS);
-                v = seq_units(s) * s.groups * a.c.n_kv_heads;
-            }
-            int64_t inc = v;
+        inc = v;
 #pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int64_t o = __shfl_up_sync(kFullMask, inc, x);
-                if (lane >= x) inc += o;
-            }
-            if (lane == 31) s_sum[warp] = inc;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) inc += s_sum[w];
-            inc += run;
-            if (threadIdx.x == kSplitWarps * 32 - 1) s_total = inc;
-            if (pass && inc - v <= u_lo && u_lo < inc) {
-                s_b = b;
-                s_before = inc - v;
-            }
-            __syncthreads();
-            run = s_total;
-            if (pass && run > u_lo) break;
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(kFullMask, inc, x);
+            if (lane >= x) inc += o;
         }
-        if (!pass) total = run;
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        inc += run;
+#pragma unroll
+        for (int w = 0; w < kSplitWarps; ++w) {
+            const int64_t o = s_sum[w];
+            if (w < warp) inc += o;
+            run += o;
+        }
+        __syncthreads();
+    };
+    for (int b0 = 0; b0 < a.d.n_seqs; b0 += kChunk) scan(b0);
+    total = run;
+    ctas = (int)min(total, (int64_t)C::CTAS);  // a unit each at least
+    if (blockIdx.x < ctas) {
+        u_lo = run_start(total, blockIdx.x, ctas);
+        u_hi = run_start(total, blockIdx.x + 1, ctas);
+        int b0 = 0;
+        if (a.d.n_seqs > kChunk) {
+            run = 0;
+            for (b0 = -kChunk; run <= u_lo;) scan(b0 += kChunk);
+        }
+        if (inc - v <= u_lo && u_lo < inc) {
+            s_b = b0 + threadIdx.x;
+            s_before = inc - v;
+        }
+        __syncthreads();
     }
     Span *spans = static_cast<Span *>(a.workspace);
     float *parts = reinterpret_cast<float *>(spans + kSplitMaxCtas);
-    if (u_lo == u_hi) {
-        if (threadIdx.x == 0) spans[blockIdx.x].parts = 0;
-        return;
-    }
-    int b = s_b;
+    if (threadIdx.x == 0) spans[blockIdx.x].parts = 0;
+    if (u_lo == u_hi) return;
+    int b = uniform(s_b);
     Seq s = seq_of(a, b, ROWS);
-    int64_t per = seq_units(s);
-    int64_t vh = (u_lo - s_before) / per;        // (KV head, row group) inside the sequence
-    int64_t first = s_before + vh * per;         // its first unit
-    int span_parts = 0, span_slot = 0, span_hk = 0, span_row0 = 0, span_t0 = 0, span_rows = 0;
+    auto settle = [&]() {
+        s.n = uniform(s.n), s.L = uniform(s.L), s.tile0 = uniform(s.tile0), s.tiles = uniform(s.tiles);
+        s.groups = uniform(s.groups);
+    };
+    settle();
+    // from here on units count from u_lo
+    int per = seq_units(s);
+    int vh = uniform((int)((u_lo - s_before) / per));  // (KV head, row group) inside the sequence
+    int first = uniform((int)(s_before + (int64_t)vh * per - u_lo));  // its first unit
+    const int units = uniform((int)(u_hi - u_lo));
+    const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)0x80000000);
+    const uint32_t ring_u = smem_u32(ring), scratch_u = smem_u32(scratch);
+    const uint32_t lane_chunk = code_chunk<D>(lane / NB, lane % NB);
 
-    for (int64_t u = u_lo; u < u_hi;) {
-        const int64_t u_end = min(first + per, u_hi);
-        const int rg = (int)(vh / a.c.n_kv_heads), hk = (int)(vh - (int64_t)rg * a.c.n_kv_heads);
+    for (int u = 0; u < units;) {
+        const int u_end = min(first + per, units);
+        const int rg = vh / a.c.n_kv_heads, hk = vh - rg * a.c.n_kv_heads;
         const int row0 = rg * ROWS;
         const int rows = min(ROWS, s.n * a.group - row0);
         const int p_first = s.L - s.n;           // position of query 0
 
         // ---- the warp's tiles: tile0 + 8 unit + warp
-        int it = s.tile0 + (int)(u - first) * kSplitWarps + warp;
-        const int t_end = min(s.tile0 + s.tiles, s.tile0 + (int)(u_end - first) * kSplitWarps);
+        int it = s.tile0 + (u - first) * kSplitWarps + warp;
+        const int t_end = min(s.tile0 + s.tiles, s.tile0 + (u_end - first) * kSplitWarps);
         const int32_t *table = a.table + (int64_t)b * a.d.max_pages;
-        const int tile_shift = a.page_shift - 4;
-        int nit = it, page = -1;                 // next tile to ask for, and its page
-        uint32_t there = 0;                      // bit s: stage s holds a tile
-        if (nit < t_end) page = __ldg(table + (nit >> tile_shift));
+        int nit = it;                            // next tile to ask for
+        uint32_t page[2] = {~0u, ~0u}, there = 0;  // the pages of its halves; bit 2 s + h: half h of stage s is there
+        auto pages = [&]() {
+            if (nit < t_end) {
+                page[0] = __ldg(table + (nit * kTile >> a.page_shift));
+                page[1] = nit * kTile + 16 < s.L ? __ldg(table + ((nit * kTile + 16) >> a.page_shift)) : ~0u;
+            } else {
+                page[0] = page[1] = ~0u;
+            }
+        };
+        pages();
         auto issue = [&](int stage) {
-            const bool ok = nit < t_end && page >= 0 && page < a.c.n_pages;
-            there = (there & ~(1u << stage)) | ((ok ? 1u : 0u) << stage);
-            if (ok) {
-                const int64_t row = (((int64_t)page * a.c.n_kv_heads + hk) << a.page_shift) +
-                                    ((nit & ((1 << tile_shift) - 1)) << 4);
-                uint8_t *st = ring + stage * C::STAGE;
-                const uint8_t *kc = static_cast<const uint8_t *>(a.c.k_codes) + row * (D / 2);
-                const uint8_t *vc = static_cast<const uint8_t *>(a.c.v_codes) + row * (D / 2);
+            const uint32_t st = ring_u + stage * C::STAGE;
+            there &= ~(3u << 2 * stage);
 #pragma unroll
-                for (int i = 0; i < (16 * NB + 31) / 32; ++i) {
-                    const int c = lane + 32 * i, r = c / NB, ch = c % NB;
-                    cp_async16(st + code_chunk<D>(r, ch), kc + c * 16);
-                    cp_async16(st + 8 * D + code_chunk<D>(r, ch), vc + c * 16);
-                }
-                if (lane < 4 * NB) {             // scales: 2 NB chunks of keys, then of values
-                    const int c = lane < 2 * NB ? lane : lane - 2 * NB;
-                    const uint8_t *sc = static_cast<const uint8_t *>(lane < 2 * NB ? a.c.k_scales : a.c.v_scales);
-                    cp_async16(st + 16 * D + lane * 16, sc + row * (D / 16) + c * 16);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t pg = uniform(page[h]);
+                if (pg < n_pages) {
+                    there |= 1u << (2 * stage + h);
+                    const uint32_t row = ((pg * a.c.n_kv_heads + hk) << a.page_shift) +
+                                         ((nit * kTile + 16 * h) & (a.c.page_size - 1));
+                    const uint8_t *kc = static_cast<const uint8_t *>(a.c.k_codes) + (uint64_t)row * (D / 2) + lane * 16;
+                    const uint8_t *vc = static_cast<const uint8_t *>(a.c.v_codes) + (uint64_t)row * (D / 2) + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < (16 * NB + 31) / 32; ++i) {
+                        // lanes 32 chunks on lie 32 / NB rows on: the shift is the same for D = 64 and 128
+                        const uint32_t to = st + h * 8 * D + (D == 256 ? code_chunk<D>(lane / NB + i * (32 / NB), lane % NB)
+                                                                       : lane_chunk + i * 512);
+                        cp_async16(to, kc + i * 512);
+                        cp_async16(to + 16 * D, vc + i * 512);
+                    }
+                    if (lane < 4 * NB) {         // scales: 2 NB chunks of keys, then of values
+                        const bool v = lane >= 2 * NB;
+                        const uint8_t *sc = static_cast<const uint8_t *>(v ? a.c.v_scales : a.c.k_scales) + lane * 16;
+                        // D bytes a half: 2 NB chunks of 16
+                        cp_async16(st + 32 * D + h * D + (v ? D : 0) + lane * 16, sc - (v ? D : 0) + (uint64_t)row * (D / 16));
+                    }
                 }
             }
             cp_async_commit();
             nit += kSplitWarps;
-            if (nit < t_end) page = __ldg(table + (nit >> tile_shift));
+            pages();
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) issue(i);
@@ -299,8 +361,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
             for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
             for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-            const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 253u);
-            const float mul = m > 0.f ? __uint_as_float((254u - ex) << 23) : 1.f;  // largest value to [1, 2)
+            const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 252u);
+            const float mul = m > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
             float corr = 0.f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -311,12 +373,17 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
             }
 #pragma unroll
             for (int x = 1; x < 32 / NB; x <<= 1) corr += __shfl_xor_sync(kFullMask, corr, x);
-            if ((lane & (32 / NB - 1)) == 0) scorr[r * NB + lane / (32 / NB)] = corr;
-            if (lane == 0) sfac[r] = a.scale_log2 * (m > 0.f ? __uint_as_float(ex << 23) : 1.f);
+            if ((lane & (32 / NB - 1)) == 0) {  // at most 1032 * 32 in magnitude
+                const __half c0 = __float2half_rn(corr);
+                scorr[r * 2 * NB + lane / (32 / NB)] = c0;
+                scorr[r * 2 * NB + NB + lane / (32 / NB)] = __float2half_rn(corr - __half2float(c0));
+            }
+            if (lane == 0) sfac[r] = a.scale_log2 * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f);
         }
         __syncthreads();
         uint32_t qf[NT][NB][4];
-        float corr[NT][NB][2], fac[NT][2], M[NT][2], l[NT][2], o[NT][2 * NB][4];
+        uint32_t cf[NT][2];
+        float fac[NT][2], M[NT][2], l[NT][2], o[NT][2 * NB][4];
         int hi[NT][2], lo[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -325,11 +392,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                 const uint4 w = *reinterpret_cast<const uint4 *>(sq + (n * 8 + g) * D + 32 * k + 8 * t);
                 qf[n][k][0] = w.x, qf[n][k][1] = w.y, qf[n][k][2] = w.z, qf[n][k][3] = w.w;
             }
+            // row n * 8 + g: offset sums of blocks 2t, 2t + 1 against the scales (D < 256: both parts in one half of k)
+            const uint32_t *sc = reinterpret_cast<const uint32_t *>(scorr + (n * 8 + g) * 2 * NB);
+            cf[n][0] = t < NB ? sc[t] : 0u;
+            cf[n][1] = NB == 8 ? sc[t + 4] : 0u;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int r = n * 8 + 2 * t + j;
-#pragma unroll
-                for (int k = 0; k < NB; ++k) corr[n][k][j] = scorr[r * NB + k];
                 fac[n][j] = sfac[r];
                 const int p = p_first + (row0 + r) / a.group;
                 hi[n][j] = min(p, s.L - 1);
@@ -347,61 +416,108 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
         const int full_hi = p_first + row0 / a.group;
         const int full_lo = a.d.window > 0 ? (int)max((int64_t)p_first + last_row - a.d.window, (int64_t)-1) : -1;
 
-        uint32_t *vs = reinterpret_cast<uint32_t *>(scratch);         // [8 key pairs][NB] half2
-        float2 *ve = reinterpret_cast<float2 *>(scratch + D);         // [16 keys] (e, 2^-e)
-        for (int stage = 0; it < t_end; it += kSplitWarps, stage = (stage + 1) & (kStages - 1)) {
-            cp_async_wait<kStages - 2>();
+        // word t of block 0 of key g; word g / 2 of block 0 of key 2t, and the half of it with values 4g .. 4g + 3
+        const uint32_t k_base = code_chunk<D>(g, 0) + 4 * t, v_base = 16 * D + code_chunk<D>(2 * t, 0) + 4 * (g >> 1);
+        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // values 4g .. 4g + 3 of a block
+        float *ve = reinterpret_cast<float *>(scratch + 2 * D);       // [32 keys] (e, 2^-e)
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int stage = 0; it < t_end; it += kSplitWarps, stage ^= 1) {
+            cp_async_wait<0>();
             __syncwarp();
-            issue((stage + kStages - 1) & (kStages - 1));
-            if (!(there >> stage & 1)) continue;
-            const uint8_t *st = ring + stage * C::STAGE;
+            issue(stage ^ 1);
+            const uint32_t have = there >> 2 * stage & 3;
+            if (!have) continue;
+            const uint32_t st = ring_u + stage * C::STAGE;
             const int j0 = it * kTile;
+            const bool full = have == 3 && j0 + kTile - 1 < s.L;
 
-            // V scales: normalised per key, in key pairs
+            // V scales in key pairs, [2][8 pairs][NB] half2
+            float2 e[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) e[h][0] = e[h][1] = make_float2(0.f, 1.f);
             {
-                const __half *sc = reinterpret_cast<const __half *>(st + 17 * D);
-                const bool in0 = j0 + 2 * g < s.L, in1 = j0 + 2 * g + 1 < s.L;
-                __half2 x[(NB + 3) / 4], m = __float2half2_rn(0.f);
+                constexpr int N = (NB + 3) / 4;
+                uint32_t x[2][N], m = 0;
 #pragma unroll
-                for (int i = 0; i < (NB + 3) / 4; ++i) {
-                    const int k = (t + 4 * i) & (NB - 1);
-                    x[i] = __halves2half2(in0 ? sc[2 * g * NB + k] : __half(0.f), in1 ? sc[(2 * g + 1) * NB + k] : __half(0.f));
-                    m = __hmax2(m, __habs2(x[i]));
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const uint32_t at = st + 34 * D + h * D + (2 * g * NB + ((t + 4 * i) & (NB - 1))) * 2;
+                        x[h][i] = lds_half(at) | lds_half(at + 2 * NB) << 16;
+                    }
+                if (!full) {  // whatever lies behind the sequence or was never copied
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = j0 + 16 * h + 2 * g;
+                        const uint32_t keep = have >> h & 1 ? (j < s.L ? 0xffffu : 0u) | (j < s.L - 1 ? 0xffff0000u : 0u) : 0u;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) x[h][i] &= keep;
+                    }
                 }
-                m = __hmax2(m, bits_h2(__shfl_xor_sync(kFullMask, h2_bits(m), 1)));
-                m = __hmax2(m, bits_h2(__shfl_xor_sync(kFullMask, h2_bits(m), 2)));
-                const uint32_t e = __vmaxu2(h2_bits(m) & 0x7c007c00u, 0x04000400u);
-                const __half2 mul = bits_h2(0x7c007c00u - e);          // 2^(1 - e)
 #pragma unroll
-                for (int i = 0; i < (NB + 3) / 4; ++i)
-                    if (t + 4 * i < NB) vs[g * NB + t + 4 * i] = h2_bits(__hmul2(x[i], mul));
-                if (t == 0) {
-                    const int e0 = (int)(e >> 10 & 31) - 15, e1 = (int)(e >> 26) - 15;
-                    *reinterpret_cast<float4 *>(ve + 2 * g) =
-                        make_float4((float)e0, __int_as_float((127 - e0) << 23), (float)e1, __int_as_float((127 - e1) << 23));
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) m = max(max(m, x[h][i] << 17), (x[h][i] & 0x7fff0000u) << 1);
+                const bool large = m >= 0x4c00u << 17, fair = m >= 0x2400u << 17;
+                const uint32_t to = scratch_u + (g * NB + t) * 4;
+                if (!__any_sync(kFullMask, large) && __any_sync(kFullMask, fair)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            if (t + 4 * i < NB) sts32(to + h * D + 16 * i, x[h][i]);
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        __half2 y = __habs2(bits_h2(x[h][0]));
+#pragma unroll
+                        for (int i = 1; i < N; ++i) y = __hmax2(y, __habs2(bits_h2(x[h][i])));
+                        y = __hmax2(y, bits_h2(__shfl_xor_sync(kFullMask, h2_bits(y), 1)));
+                        y = __hmax2(y, bits_h2(__shfl_xor_sync(kFullMask, h2_bits(y), 2)));
+                        const uint32_t z = __vmaxu2(h2_bits(y) & 0x7c007c00u, 0x04000400u);
+                        const __half2 mul = bits_h2(0x7c007c00u - z);  // 2^(1 - exponent)
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            if (t + 4 * i < NB) sts32(to + h * D + 16 * i, h2_bits(__hmul2(bits_h2(x[h][i]), mul)));
+                        if (t == 0) {
+                            const int f0 = (int)(z >> 10 & 31) - 16, f1 = (int)(z >> 26) - 16;  // s 2^-f in [2, 4)
+                            *reinterpret_cast<float4 *>(ve + 32 * h + 4 * g) =
+                                make_float4((float)f0, __int_as_float((127 - f0) << 23), (float)f1,
+                                            __int_as_float((127 - f1) << 23));
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) e[h][r] = *reinterpret_cast<float2 *>(ve + 32 * h + 2 * g + 16 * r);
                 }
             }
             // S^T
-            float x[NT][4];
-            {
+            float x[NT][2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 float ks[2][NB];
+                const uint32_t sc = st + 32 * D + h * D + g * NB * 2;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const __half2 *sc = reinterpret_cast<const __half2 *>(st + 16 * D + (g + 8 * r) * NB * 2);
                     uint32_t w[NB / 2];
-                    if constexpr (NB == 2) w[0] = *reinterpret_cast<const uint32_t *>(sc);
-                    if constexpr (NB == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(sc);
-                    if constexpr (NB == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(sc);
+                    lds_words(sc + r * 16 * NB, w);
 #pragma unroll
                     for (int k = 0; k < NB / 2; ++k) {
                         const float2 f = __half22float2(bits_h2(w[k]));
                         ks[r][2 * k] = f.x, ks[r][2 * k + 1] = f.y;
                     }
                 }
+                const uint32_t s0 = lds32(sc + (2 * t & (NB - 1)) * 2), s1 = lds32<16 * NB>(sc + (2 * t & (NB - 1)) * 2);
+                const uint32_t as[4] = {s0, s1, NB == 8 ? s0 : 0u, NB == 8 ? s1 : 0u};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(x[n][h], as, cf[n][0], cf[n][1], zero);
+                const uint32_t base = st + k_base + h * 8 * D;
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(st + code_chunk<D>(g, k) + 4 * t);
-                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(st + code_chunk<D>(g + 8, k) + 4 * t);
+                    const uint32_t w0 = lds32(base ^ (16 * k)), w1 = lds32<4 * D>(base ^ (16 * k));
                     const uint32_t a0[4] = {and_or(w0, 0x000f000fu, 0x64006400u), and_or(w1, 0x000f000fu, 0x64006400u),
                                             and_or(w0, 0x00f000f0u, 0x54005400u), and_or(w1, 0x00f000f0u, 0x54005400u)};
                     const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
@@ -410,39 +526,44 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float c[4];
-                        const float c0[4] = {corr[n][k][0], corr[n][k][1], corr[n][k][0], corr[n][k][1]};
-                        mma16816(c, a0, qf[n][k][0], qf[n][k][1], c0);
+                        mma16816(c, a0, qf[n][k][0], qf[n][k][1], zero);
                         mma16816(c, a1, qf[n][k][2], qf[n][k][3], c);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[n][j] = k ? fmaf(c[j], ks[j >> 1][k], x[n][j]) : c[j] * ks[j >> 1][k];
+                        for (int j = 0; j < 4; ++j) x[n][h][j] = fmaf(c[j], ks[j >> 1][k], x[n][h][j]);
                     }
                 }
             }
-            __syncwarp();
-            // softmax: weights of keys g, g + 8 for query rows 2t, 2t + 1
-            const float2 e0 = ve[g], e1 = ve[g + 8];
-            const bool whole = j0 + kTile - 1 <= full_hi && j0 > full_lo;
+            // softmax: weights of keys g, g + 8 of each half for query rows 2t, 2t + 1
+            const bool whole = full && j0 + kTile - 1 <= full_hi && j0 > full_lo;
             bool grow = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[n][j] = fmaf(x[n][j], fac[n][j & 1], j < 2 ? e0.x : e1.x);
-                    if (!whole) {
-                        const int pos = j0 + g + (j < 2 ? 0 : 8);
-                        if (pos > hi[n][j & 1] || pos <= lo[n][j & 1]) x[n][j] = -INFINITY;
-                    }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[n][h][j] = fmaf(x[n][h][j], fac[n][j & 1], e[h][j >> 1].x);
+                if (!whole) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int pos = j0 + 16 * h + g + (j < 2 ? 0 : 8);
+                            if (pos > hi[n][j & 1] || pos <= lo[n][j & 1] || !(have >> h & 1)) x[n][h][j] = -INFINITY;
+                        }
                 }
-                grow |= fmaxf(x[n][0], x[n][2]) > M[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) > M[n][1] + 8.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    grow |= fmaxf(fmaxf(x[n][0][j], x[n][0][j + 2]), fmaxf(x[n][1][j], x[n][1][j + 2])) > M[n][j] + 11.f;
             }
             if (__any_sync(kFullMask, grow)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float m = fmaxf(M[n][j], fmaxf(x[n][j], x[n][j + 2]));
+                        float m = fmaxf(fmaxf(x[n][0][j], x[n][0][j + 2]), fmaxf(x[n][1][j], x[n][1][j + 2]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
+                        m = fmaxf(M[n][j], m - 6.f);
                         const float f = ex2(M[n][j] - m);
                         M[n][j] = m;
                         l[n][j] *= f;
@@ -450,47 +571,52 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                         for (int k = 0; k < 2 * NB; ++k) o[n][k][j] *= f, o[n][k][j + 2] *= f;
                     }
             }
-            uint32_t p0[NT], p1[NT];
+            uint32_t pr[NT][2][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[n][j] = ex2(x[n][j] - M[n][j & 1]);
-                    l[n][j & 1] = fmaf(x[n][j], j < 2 ? e0.y : e1.y, l[n][j & 1]);
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[n][h][j] = ex2(x[n][h][j] - M[n][j & 1]);
+                        l[n][j & 1] = fmaf(x[n][h][j], e[h][j >> 1].y, l[n][j & 1]);
+                    }
+                    pr[n][h][0] = transpose8x8(h2_bits(__floats2half2_rn(x[n][h][0], x[n][h][1])));  // keys 2t, 2t + 1
+                    pr[n][h][1] = transpose8x8(h2_bits(__floats2half2_rn(x[n][h][2], x[n][h][3])));  // keys 2t + 8, 2t + 9
                 }
-                p0[n] = transpose8x8(h2_bits(__floats2half2_rn(x[n][0], x[n][1])));  // keys 2t, 2t + 1
-                p1[n] = transpose8x8(h2_bits(__floats2half2_rn(x[n][2], x[n][3])));  // keys 2t + 8, 2t + 9
-            }
             // O^T
-            const uint8_t *vt = st + 8 * D + 4 * (g >> 1);
-            const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // values 4g .. 4g + 3 of a block
             const __half2 off = __floats2half2_rn(-1032.f, -1032.f), off64 = __floats2half2_rn(-72.f, -72.f);
             auto unpack = [&](uint32_t w, uint32_t (&v)[4]) {
-                const uint32_t h = w >> 8;
+                const uint32_t u = w >> 8;
                 v[0] = h2_bits(__hadd2(bits_h2(and_or(w, 0x000f000fu, 0x64006400u)), off));
                 v[1] = h2_bits(__hadd2(bits_h2(and_or(w, 0x00f000f0u, 0x54005400u)), off64));
-                v[2] = h2_bits(__hadd2(bits_h2(and_or(h, 0x000f000fu, 0x64006400u)), off));
-                v[3] = h2_bits(__hadd2(bits_h2(and_or(h, 0x00f000f0u, 0x54005400u)), off64));
+                v[2] = h2_bits(__hadd2(bits_h2(and_or(u, 0x000f000fu, 0x64006400u)), off));
+                v[3] = h2_bits(__hadd2(bits_h2(and_or(u, 0x00f000f0u, 0x54005400u)), off64));
             };
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                uint32_t w[4];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t vs0[NB], vs1[NB];
+                lds_words(scratch_u + h * D + t * NB * 4, vs0);
+                lds_words(scratch_u + h * D + (t + 4) * NB * 4, vs1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = *reinterpret_cast<const uint32_t *>(vt + code_chunk<D>(2 * t + (j & 1) + (j >> 1) * 8, k));
-                uint32_t v0[4], v1[4];
-                unpack(__byte_perm(w[0], w[1], sel), v0);
-                unpack(__byte_perm(w[2], w[3], sel), v1);
-                const __half2 s0 = bits_h2(vs[t * NB + k]), s1 = bits_h2(vs[(t + 4) * NB + k]);
-                const uint32_t a0[4] = {v0[0], v0[1], v1[0], v1[1]}, a1[4] = {v0[2], v0[3], v1[2], v1[3]};
+                for (int k = 0; k < NB; ++k) {
+                    // keys 2t, 2t + 1 and 8 on
+                    const uint32_t at = (st + v_base + h * 8 * D) ^ (16 * k), at1 = (D == 256 ? at ^ 16 : at) + D / 2;
+                    const uint32_t w[4] = {lds32(at), lds32(at1), lds32<4 * D>(at), lds32<4 * D>(at1)};
+                    uint32_t v0[4], v1[4];
+                    unpack(__byte_perm(w[0], w[1], sel), v0);
+                    unpack(__byte_perm(w[2], w[3], sel), v1);
+                    const uint32_t a0[4] = {v0[0], v0[1], v1[0], v1[1]}, a1[4] = {v0[2], v0[3], v1[2], v1[3]};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint32_t b0 = h2_bits(__hmul2(bits_h2(p0[n]), s0)), b1 = h2_bits(__hmul2(bits_h2(p1[n]), s1));
-                    mma16816(o[n][2 * k], a0, b0, b1, o[n][2 * k]);
-                    mma16816(o[n][2 * k + 1], a1, b0, b1, o[n][2 * k + 1]);
+                    for (int n = 0; n < NT; ++n) {
+                        const uint32_t b0 = h2_bits(__hmul2(bits_h2(pr[n][h][0]), bits_h2(vs0[k]))),
+                                       b1 = h2_bits(__hmul2(bits_h2(pr[n][h][1]), bits_h2(vs1[k])));
+                        mma16816(o[n][2 * k], a0, b0, b1, o[n][2 * k]);
+                        mma16816(o[n][2 * k + 1], a1, b0, b1, o[n][2 * k + 1]);
+                    }
                 }
             }
-            __syncwarp();  // the scratch and the stage are written again
+            __syncwarp();  // the scratch is written again
         }
         cp_async_wait<0>();
         __syncwarp();
@@ -516,7 +642,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
             }
         __syncthreads();
         const bool whole = u == first && u_end == first + per;
-        const int slot = u == u_lo ? 0 : 1;
+        const int slot = u ? 1 : 0;
         for (int r = warp; r < rows; r += kSplitWarps) {
             float m = sM[r];
 #pragma unroll
@@ -541,73 +667,85 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                 if (lane == 0) part[D] = m, part[D + 1] = sum;
             }
         }
-        if (u == first && u_end < first + per) {
+        if (u == first && !whole && threadIdx.x == 0) {
             // it starts here and ends in the CTA that holds its last unit
-            const int64_t last = first + per - 1;
+            const int64_t last = u_lo + first + per - 1;
             int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
             while (run_start(total, c + 1, ctas) <= last) ++c;
-            span_parts = c - blockIdx.x + 1;
-            span_slot = slot, span_hk = hk, span_row0 = row0, span_t0 = (int)s.t0, span_rows = rows;
+            spans[blockIdx.x] = Span{c - (int)blockIdx.x + 1, slot, (int)s.t0, rows, hk, row0, {0, 0}};
         }
         __syncthreads();
         u = u_end;
-        if (u < u_hi) {
+        if (u < units) {
             first += per;
-            if (++vh == (int64_t)s.groups * a.c.n_kv_heads) {
+            if (++vh == s.groups * a.c.n_kv_heads) {
                 vh = 0;
                 do {
                     s = seq_of(a, ++b, ROWS);
                 } while (s.groups == 0);
+                settle();
                 per = seq_units(s);
             }
         }
     }
-    if (threadIdx.x == 0) spans[blockIdx.x] = Span{span_parts, span_slot, span_t0, span_rows, span_hk, span_row0, {0, 0}};
 }
 
-// One block for each query row of a piece that several CTAs share: 8 warps
-// over its parts, then over each other, in a fixed order.
+// One block for each piece that several CTAs share and two of its query rows:
+// eight warps over the parts of a row, then over each other, in a fixed order.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
     constexpr int P = D / 32, PART = D + 4;
-    __shared__ float so[8][D], sl[8], sm[8];
+    __shared__ float so[8][2][D], sl[8][2], sw[2][kSplitMaxCtas];
     griddep_wait();
     const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
-    const int r = blockIdx.y;
-    if (sp.parts == 0 || r >= sp.rows) return;
+    if (sp.parts == 0) return;
     const float *parts = reinterpret_cast<const float *>(static_cast<const Span *>(a.workspace) + kSplitMaxCtas);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wr = warp & 1, wq = warp >> 1, r = blockIdx.y * 2 + wr;
+    const bool live = r < sp.rows;
     auto at = [&](int i) {
         return parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
     };
     float m = -FLT_MAX;
-    for (int i = threadIdx.x; i < sp.parts; i += 256) m = fmaxf(m, at(i)[D]);
+    if (live)
+        for (int i = lane; i < sp.parts; i += 32) m = fmaxf(m, at(i)[D]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-    if (lane == 0) sm[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, sm[w]);
     float v[P], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < P; ++j) v[j] = 0.f;
-    for (int i = warp; i < sp.parts; i += 8) {
-        const float *p = at(i);
-        const float f = ex2(p[D] - m);
-        sum = fmaf(p[D + 1], f, sum);
+    if (live) {
+        for (int i = wq + 8 * lane; i < sp.parts; i += 256) {  // the parts of this warp
+            const float f = ex2(at(i)[D] - m);
+            sw[wr][i] = f;
+            sum = fmaf(at(i)[D + 1], f, sum);
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = wq; i < sp.parts; i += 8) {
+            const float f = sw[wr][i];
+            float w[P];
+            if constexpr (P == 2) *reinterpret_cast<float2 *>(w) = *reinterpret_cast<const float2 *>(at(i) + lane * P);
+            if constexpr (P >= 4)
 #pragma unroll
-        for (int j = 0; j < P; ++j) v[j] = fmaf(p[lane * P + j], f, v[j]);
+                for (int j = 0; j < P; j += 4)
+                    *reinterpret_cast<float4 *>(w + j) = *reinterpret_cast<const float4 *>(at(i) + lane * P + j);
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = fmaf(w[j], f, v[j]);
+        }
     }
 #pragma unroll
-    for (int j = 0; j < P; ++j) so[warp][lane * P + j] = v[j];
-    if (lane == 0) sl[warp] = sum;
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFullMask, sum, x);
+#pragma unroll
+    for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
+    if (lane == 0) sl[wq][wr] = sum;
     __syncthreads();
-    if (warp) return;
+    if (wq || !live) return;
 #pragma unroll
     for (int w = 1; w < 8; ++w) {
-        sum += sl[w];
+        sum += sl[w][wr];
 #pragma unroll
-        for (int j = 0; j < P; ++j) v[j] += so[w][lane * P + j];
+        for (int j = 0; j < P; ++j) v[j] += so[w][wr][lane * P + j];
     }
     store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
 }
@@ -622,8 +760,8 @@ cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t s
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C::CTAS, C::ROWS);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(C::CTAS, C::ROWS / 2);
+    cfg.blockDim = dim3(512);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
