@@ -11,7 +11,7 @@ OUT = os.path.join(HERE, "libstrata_moe.so")
 # the same sources with every data-derived index bounds-checked into the status word
 OUT_CHECKED = os.path.join(HERE, "libstrata_moe_checked.so")
 SOURCES = ["strata_moe.cu", "route.cu", "decode_fused.cu", "prefill_gemm.cu", "misc.cu", "route_noalloc.cu", "router_gemm.cu", "kv_codec.cu", "rope.cu", "kv_pages.cu",
-           "kv_attention.cu"]
+           "kv_attention.cu", "kv_attn_tiles.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
          "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr", "--threads", "0"]

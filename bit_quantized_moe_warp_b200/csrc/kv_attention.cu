@@ -5,47 +5,15 @@
 // for the stored row y = (c - 8) s, and sum_j p_j v'_j = H (sum_j p_j y_j) / sqrt D:
 // a query row is rotated once on the way in and its output once on the way
 // out, and the cache's rows are used as they are stored.
-#include <cfloat>
 #include <cmath>
 
 #include "abi_internal.h"
-#include "common.cuh"
-#include "kv4_row.cuh"
+#include "kv_attn.cuh"
 
 using namespace strata;
 
 namespace {
 
-struct AttnArgs {
-    strata_kv4_cache c;
-    strata_kv4_attn_desc d;
-    const int32_t *positions;
-    const __nv_bfloat16 *q;
-    const int32_t *q_offsets, *kv_lens, *table;
-    __nv_bfloat16 *out;
-    void *workspace;
-    int group, page_shift;
-    float scale_log2;  // scale * log2(e)
-};
-
-// Row r of a KV head's query rows (token-major, the group's heads inside), in
-// the rotated basis: back through the transform, divided by its sum, rounded
-// once.
-template <int D>
-__device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32], float l, int64_t t0, int hk, int r,
-                                          int lane) {
-    constexpr int P = D / 32;
-    const int i = r / a.group, h = hk * a.group + r - i * a.group;
-    const float f = l > 0.f ? rsqrt_dim<D>() / l : 0.f;
-    fwht_warp<D>(v, lane);
-    uint32_t w[P / 2];
-#pragma unroll
-    for (int j = 0; j < P / 2; ++j) w[j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
-    uint8_t *dst = reinterpret_cast<uint8_t *>(a.out + (t0 + i) * a.d.out_token_stride + (int64_t)h * D + lane * P);
-    if constexpr (P == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
-    if constexpr (P == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    if constexpr (P == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // ---------------------------------------------------------------- few rows
 // k_attn_split: up to 8 NT query rows of a KV head (tokens x heads of the
@@ -73,19 +41,10 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32],
 // any mix of lengths fills the machine. A run that covers a sequence's whole
 // cache writes its rows; the others leave (M, l, O) in the workspace, two at
 // most for a CTA, and k_attn_join adds them up in a fixed order.
-constexpr int kSms = 148;
 constexpr int kSplitParts = 2 * 16 * kSms;  // rows of partial results: 2 x 8 rows x 296 CTAs or 2 x 16 x 148
-constexpr int kSplitMaxCtas = 2 * kSms;
 constexpr int kSplitWarps = 8;
 constexpr int kStages = 2;  // a warp's own work on a tile covers the latency of the next
 constexpr int kTile = 32;   // keys, as two halves of 16: no half crosses a page
-
-struct Span {  // what k_attn_join needs of the last piece of a CTA
-    int parts;  // CTAs that share it, 0: none
-    int slot;   // of the first one; 0 for the others
-    int t0, rows, hk, row0;
-    int pad[2];
-};
 
 template <int D, int NT>
 struct Split {
@@ -104,11 +63,6 @@ struct Split {
     static_assert(2 * ROWS * CTAS <= kSplitParts && CTAS <= kSplitMaxCtas, "workspace");
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -175,19 +129,12 @@ __device__ __forceinline__ int code_chunk(int r, int c) {
 // Within 16-key tiles x(r + 8) = x(r), and for even r x(r + 1) = x(r) (^ 1 for
 // D = 256): a lane needs one address, one XOR for each block.
 
-// A value that is the same in every lane, so that the compiler sees it is:
-// branches on it need no reconvergence
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFullMask, v, 0); }
-
-struct Seq {  // one sequence as the kernels see it
-    int64_t t0;
-    int n, L, tile0, tiles, groups;
+struct Seq : SeqBase {
+    int tile0, tiles, groups;
 };
 __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_group) {
     Seq s;
-    s.t0 = min(max((int64_t)a.q_offsets[b], (int64_t)0), a.d.n_tokens);
-    s.n = (int)(min(max((int64_t)a.q_offsets[b + 1], s.t0), a.d.n_tokens) - s.t0);
-    s.L = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.d.max_pages << a.page_shift);
+    load_seq(s, a, b);
     const int64_t first = a.d.window > 0 ? max((int64_t)0, (int64_t)s.L - s.n - a.d.window + 1) : 0;
     s.tile0 = (int)(min(first, (int64_t)s.L) / kTile);
     s.tiles = (int)(((int64_t)s.L + kTile - 1) / kTile) - s.tile0;
@@ -197,11 +144,6 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_gro
 // units of one (KV head, row group); one at least, which writes the zeros of a
 // sequence without keys
 __device__ __forceinline__ int seq_units(const Seq &s) { return max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
-
-// total * i / n, rounded down: where run i of n starts
-__device__ __forceinline__ int64_t run_start(int64_t total, int64_t i, int64_t n) {
-    return (int64_t)((uint64_t)total * (uint64_t)i / (uint64_t)n);
-}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
@@ -690,82 +632,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
     }
 }
 
-// One block for each piece that several CTAs share and two of its query rows:
-// eight warps over the parts of a row, then over each other, in a fixed order.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
-    constexpr int P = D / 32, PART = D + 4;
-    __shared__ float so[8][2][D], sl[8][2], sw[2][kSplitMaxCtas];
-    griddep_wait();
-    const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
-    if (sp.parts == 0) return;
-    const float *parts = reinterpret_cast<const float *>(static_cast<const Span *>(a.workspace) + kSplitMaxCtas);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wr = warp & 1, wq = warp >> 1, r = blockIdx.y * 2 + wr;
-    const bool live = r < sp.rows;
-    auto at = [&](int i) {
-        return parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
-    };
-    float m = -FLT_MAX;
-    if (live)
-        for (int i = lane; i < sp.parts; i += 32) m = fmaxf(m, at(i)[D]);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-    float v[P], sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < P; ++j) v[j] = 0.f;
-    if (live) {
-        for (int i = wq + 8 * lane; i < sp.parts; i += 256) {  // the parts of this warp
-            const float f = ex2(at(i)[D] - m);
-            sw[wr][i] = f;
-            sum = fmaf(at(i)[D + 1], f, sum);
-        }
-        __syncwarp();
-#pragma unroll 4
-        for (int i = wq; i < sp.parts; i += 8) {
-            const float f = sw[wr][i];
-            float w[P];
-            if constexpr (P == 2) *reinterpret_cast<float2 *>(w) = *reinterpret_cast<const float2 *>(at(i) + lane * P);
-            if constexpr (P >= 4)
-#pragma unroll
-                for (int j = 0; j < P; j += 4)
-                    *reinterpret_cast<float4 *>(w + j) = *reinterpret_cast<const float4 *>(at(i) + lane * P + j);
-#pragma unroll
-            for (int j = 0; j < P; ++j) v[j] = fmaf(w[j], f, v[j]);
-        }
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFullMask, sum, x);
-#pragma unroll
-    for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
-    if (lane == 0) sl[wq][wr] = sum;
-    __syncthreads();
-    if (wq || !live) return;
-#pragma unroll
-    for (int w = 1; w < 8; ++w) {
-        sum += sl[w][wr];
-#pragma unroll
-        for (int j = 0; j < P; ++j) v[j] += so[w][wr][lane * P + j];
-    }
-    store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
-}
-
 template <int D, int NT>
 cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     using C = Split<D, NT>;
     const cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     k_attn_split<D, NT><<<C::CTAS, kSplitWarps * 32, C::SMEM, st>>>(tab, a);
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C::CTAS, C::ROWS / 2);
-    cfg.blockDim = dim3(512);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<D, C::ROWS>, a);
+    return launch_join<D, C::ROWS>(a, C::CTAS, st);
 }
 
 }  // namespace
@@ -773,7 +646,8 @@ cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t s
 extern "C" size_t strata_kv4_attention_workspace_bytes(const strata_kv4_cache *cache, int32_t n_q_heads) {
     if (strata_check_kv4_cache(cache) != STRATA_OK) return 0;
     if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return 0;
-    return sizeof(Span) * kSplitMaxCtas + sizeof(float) * (cache->head_dim + 4) * kSplitParts;
+    const size_t split = sizeof(float) * (cache->head_dim + 4) * kSplitParts, tiles = attn_tiles_part_bytes(cache->head_dim);
+    return sizeof(Span) * kSplitMaxCtas + (split > tiles ? split : tiles);
 }
 
 extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, const strata_kv4_attn_desc *d,
@@ -820,7 +694,9 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool two = (int64_t)d->max_q_len * a.group > 8;
     cudaError_t e;
-    if (cache->head_dim == 64)
+    if ((int64_t)d->max_q_len * a.group > 16)
+        e = launch_attn_tiles(tab, a, st);
+    else if (cache->head_dim == 64)
         e = two ? launch_split<64, 2>(tab, a, st) : launch_split<64, 1>(tab, a, st);
     else if (cache->head_dim == 128)
         e = two ? launch_split<128, 2>(tab, a, st) : launch_split<128, 1>(tab, a, st);

@@ -1,0 +1,164 @@
+// kv_attn.cuh -- what the attention kernels over the paged 4-bit cache share:
+// their arguments, the division of work over CTAs, and the kernel that joins
+// partial results.
+#pragma once
+
+#include <cfloat>
+#include <math.h>
+
+#include "common.cuh"
+#include "kv4_row.cuh"
+
+namespace strata {
+
+struct AttnArgs {
+    strata_kv4_cache c;
+    strata_kv4_attn_desc d;
+    const int32_t *positions;
+    const __nv_bfloat16 *q;
+    const int32_t *q_offsets, *kv_lens, *table;
+    __nv_bfloat16 *out;
+    void *workspace;
+    int group, page_shift;
+    float scale_log2;  // scale * log2(e)
+};
+// Row r of a KV head's query rows (token-major, the group's heads inside), in
+// the rotated basis: back through the transform, divided by its sum, rounded
+// once.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32], float l, int64_t t0, int hk, int r,
+                                          int lane) {
+    constexpr int P = D / 32;
+    const int i = r / a.group, h = hk * a.group + r - i * a.group;
+    const float f = l > 0.f ? rsqrt_dim<D>() / l : 0.f;
+    fwht_warp<D>(v, lane);
+    uint32_t w[P / 2];
+#pragma unroll
+    for (int j = 0; j < P / 2; ++j) w[j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
+    uint8_t *dst = reinterpret_cast<uint8_t *>(a.out + (t0 + i) * a.d.out_token_stride + (int64_t)h * D + lane * P);
+    if constexpr (P == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if constexpr (P == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    if constexpr (P == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A value that is the same in every lane, so that the compiler sees it is:
+// branches on it need no reconvergence
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFullMask, v, 0); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// total * i / n, rounded down: where run i of n starts
+__device__ __forceinline__ int64_t run_start(int64_t total, int64_t i, int64_t n) {
+    return (int64_t)((uint64_t)total * (uint64_t)i / (uint64_t)n);
+}
+
+// A sequence: its first query row, query rows and cached tokens, in range
+struct SeqBase {
+    int64_t t0;
+    int n, L;
+};
+__device__ __forceinline__ void load_seq(SeqBase &s, const AttnArgs &a, int b) {
+    s.t0 = min(max((int64_t)a.q_offsets[b], (int64_t)0), a.d.n_tokens);
+    s.n = (int)(min(max((int64_t)a.q_offsets[b + 1], s.t0), a.d.n_tokens) - s.t0);
+    s.L = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.d.max_pages << a.page_shift);
+}
+
+constexpr int kSms = 148;
+constexpr int kSplitMaxCtas = 2 * kSms;
+
+struct Span {  // what k_attn_join needs of the last piece of a CTA
+    int parts;  // CTAs that share it, 0: none
+    int slot;   // of the first one; 0 for the others
+    int t0, rows, hk, row0;
+    int pad[2];
+};
+
+// One block for each piece that several CTAs share and two of its query rows:
+// eight warps over the parts of a row, then over each other, in a fixed order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
+    constexpr int P = D / 32, PART = D + 4;
+    __shared__ float so[8][2][D], sl[8][2], sw[2][kSplitMaxCtas];
+    griddep_wait();
+    const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
+    if (sp.parts == 0) return;
+    const float *parts = reinterpret_cast<const float *>(static_cast<const Span *>(a.workspace) + kSplitMaxCtas);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wr = warp & 1, wq = warp >> 1;
+    for (int r0 = 2 * blockIdx.y; r0 < sp.rows; r0 += 2 * gridDim.y) {
+        const int r = r0 + wr;
+        const bool live = r < sp.rows;
+        auto at = [&](int i) {
+            return parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
+        };
+        float m = -FLT_MAX;
+        if (live)
+            for (int i = lane; i < sp.parts; i += 32) m = fmaxf(m, at(i)[D]);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
+        float v[P], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] = 0.f;
+        if (live) {
+            for (int i = wq + 8 * lane; i < sp.parts; i += 256) {  // the parts of this warp
+                const float f = ex2(at(i)[D] - m);
+                sw[wr][i] = f;
+                sum = fmaf(at(i)[D + 1], f, sum);
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int i = wq; i < sp.parts; i += 8) {
+                const float f = sw[wr][i];
+                float w[P];
+                if constexpr (P == 2) *reinterpret_cast<float2 *>(w) = *reinterpret_cast<const float2 *>(at(i) + lane * P);
+                if constexpr (P >= 4)
+#pragma unroll
+                    for (int j = 0; j < P; j += 4)
+                        *reinterpret_cast<float4 *>(w + j) = *reinterpret_cast<const float4 *>(at(i) + lane * P + j);
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[j] = fmaf(w[j], f, v[j]);
+            }
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFullMask, sum, x);
+#pragma unroll
+        for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
+        if (lane == 0) sl[wq][wr] = sum;
+        __syncthreads();
+        if (wq == 0 && live) {
+#pragma unroll
+            for (int w = 1; w < 8; ++w) {
+                sum += sl[w][wr];
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[j] += so[w][wr][lane * P + j];
+            }
+            store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int ROWS>
+cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
+    // programmatic launch: the blocks come up while the last CTAs finish
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t rows = (int64_t)a.d.max_q_len * a.group;  // a hint only: a block takes more rows in turn
+    cfg.gridDim = dim3(ctas, rows < 2 ? 1 : rows < ROWS ? (unsigned)(rows + 1) / 2 : ROWS / 2);
+    cfg.blockDim = dim3(512);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_join<D, ROWS>, a);
+}
+
+// Many query rows (kv_attn_tiles.cu): bytes of its partial results, and the launch
+size_t attn_tiles_part_bytes(int head_dim);
+cudaError_t launch_attn_tiles(const RopeTable &tab, const AttnArgs &a, cudaStream_t st);
+
+}  // namespace strata

@@ -1,0 +1,759 @@
+// kv_attn_tiles.cu -- attention over the paged 4-bit cache for many query rows
+// (prompt chunks, verify steps) on the 5th-generation tensor cores.
+//
+// An item is a KV head of a sequence and up to 256 of its query rows (token-
+// major, the group's heads inside; 128 for head_dim 256) against the keys that
+// they see, in tiles of 128 keys (64 for head_dim 256). For each tile
+//   8 warps expand the packed rows into fp16 (c - 8) s, keys and values, in
+//     shared memory (128-byte swizzle), from registers loaded a tile ahead;
+//   1 thread issues S = Q K^T and O += P V (tcgen05; S, P and O in tensor
+//     memory, P in the columns of its S);
+//   8 warps turn S into P: a thread per row, so that maximum and sum need no
+//     exchange between lanes.
+// Two S stand in tensor memory, of two 128-row halves of the item; where the
+// item has at most 128 rows, of every second key tile instead, each with an O
+// of its own, added up at the end (head_dim 256: one O, S of two tiles). So the
+// tensor cores work on one while the softmax works on the other. Bound by the
+// exponentials (16 a cycle and SM) and the matrix products (4 D multiply-adds
+// a score), which take the same time at head_dim 128.
+//
+// Softmax: weights 2^(x - M + 6), M a row's running maximum, moved only when a
+// weight would pass 2^11 (then O is scaled in tensor memory). fp16 range of the
+// scales: as long as 32 keys' scales are all below 2^12 with some above 2^-10,
+// (c - 8) s is a plain fp16 product. Where not, each of these keys is
+// normalised by its own power of two, which the softmax takes back: the key's
+// as a factor of its scores, the value's as an exponent added to x.
+//
+// Work: the key tiles of all items in a row, cut into 148 equal runs, one for
+// each CTA; pieces of an item that several CTAs share go through k_attn_join.
+#include "kv_attn.cuh"
+
+namespace strata {
+namespace {
+
+constexpr int kThreads = 17 * 32;
+constexpr int kMmaWarp = 16;
+constexpr int kInfo = 4;  // tiles whose flags are kept
+
+template <int D>
+struct Tiles {
+    static constexpr int NB = D / 32;
+    static constexpr int TK = D == 256 ? 64 : 128;      // keys of a tile
+    static constexpr int SLOTS = D == 256 ? 1 : 2;      // O accumulators
+    static constexpr int ROWS = 128 * SLOTS;            // of an item
+    static constexpr int KV = TK * D * 2;               // bytes of a tile's keys in fp16
+    static constexpr int Q = 128 * D * 2;               // of 128 query rows
+    static constexpr int PART = D + 4;
+    static constexpr int O_COL = 256;                   // tensor memory: S at 0 and 128, then O
+    static constexpr int S_STEP = 128;
+    static constexpr int KMUL = 0, VE = KMUL + kInfo * TK * 4, VINV = VE + kInfo * TK * 4, FLAGS = VINV + kInfo * TK * 4,
+                         FAC = FLAGS + kInfo * 8 * 4, ML = FAC + ROWS * 4, AUX = ML + 128 * 8;
+    static constexpr int SMEM = 1024 + SLOTS * Q + 4 * KV + AUX;
+    static constexpr int SPLIT = D == 256 ? 2 : 1;      // threads for a row of codes
+    static constexpr int NW = NB / SPLIT;               // 16-byte words of codes of a thread: a block each
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(128 * D * 4 <= 4 * KV, "the second O fits the tiles' buffers");
+};
+
+STRATA_DEV void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 32 lanes x 32 bits, 32 consecutive columns per thread
+STRATA_DEV void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+STRATA_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+STRATA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+STRATA_DEV void named_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// Operand with the other dimension contiguous (V: 64 values of a key, 128-byte
+// swizzle): groups of 8 keys 1024 bytes apart, blocks of 64 values `block` apart.
+STRATA_DEV uint64_t umma_desc_sw128_mn(const void *tile, uint32_t block) {
+    uint64_t a = smem_u32(tile);
+    return ((a >> 4) & 0x3FFFull) | ((uint64_t)(block >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+STRATA_DEV uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+STRATA_DEV float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+STRATA_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+STRATA_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+STRATA_DEV uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+    return r;
+}
+STRATA_DEV uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+STRATA_DEV __half2 bits_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+
+// Where 16-byte chunk c (8 values) of row r lies: blocks of 64 values, 128-byte swizzle
+STRATA_DEV uint32_t sw_chunk(int rows, int r, int c) { return (c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+
+// Inside 8 values the chunks hold 0 4 1 5 2 6 3 7: the order of a code word's nibble pairs
+__host__ __device__ constexpr int place_of(int n) { return n < 4 ? 2 * n : 2 * n - 7; }
+__host__ __device__ constexpr int value_at(int p) { return p & 1 ? 4 + (p >> 1) : p >> 1; }
+
+struct Item {  // up to ROWS query rows of a KV head
+    int rows, row0, tile0, tiles;  // key tiles
+};
+template <int D>
+STRATA_DEV Item item_of(const AttnArgs &a, const SeqBase &s, int rt) {
+    using C = Tiles<D>;
+    Item it;
+    it.row0 = rt * C::ROWS;
+    it.rows = min(C::ROWS, s.n * a.group - it.row0);
+    const int first = it.row0 / a.group, last = (it.row0 + it.rows - 1) / a.group;
+    const int hi = max(s.L - s.n + last + 1, 0);
+    const int lo = a.d.window > 0 ? (int)max((int64_t)0, (int64_t)s.L - s.n + first - a.d.window + 1) : 0;
+    it.tile0 = min(lo, hi) / C::TK;
+    it.tiles = (int)(((int64_t)hi + C::TK - 1) / C::TK) - it.tile0;
+    return it;
+}
+// units of an item; one at least, which writes the zeros of rows without keys
+STRATA_DEV int item_units(const Item &it) { return max(it.tiles, 1); }
+
+STRATA_DEV int item_count(const AttnArgs &a, int n, int rows) { return (int)(((int64_t)n * a.group + rows - 1) / rows); }
+
+// Units of one KV head of a sequence, by a whole warp
+template <int D>
+STRATA_DEV int64_t head_units(const AttnArgs &a, const SeqBase &s, int lane) {
+    const int count = item_count(a, s.n, Tiles<D>::ROWS);
+    int64_t v = 0;
+    for (int rt = lane; rt < count; rt += 32) v += item_units(item_of<D>(a, s, rt));
+#pragma unroll
+    for (int x = 16; x; x >>= 1) v += __shfl_xor_sync(kFullMask, v, x);
+    return v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_tiles(const __grid_constant__ RopeTable tab, const __grid_constant__ AttnArgs a) {
+    using C = Tiles<D>;
+    constexpr int NB = C::NB, TK = C::TK, P = D / 32, SLOTS = C::SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sq = smem, *sk = sq + SLOTS * C::Q, *sv = sk + 2 * C::KV, *aux = sv + 2 * C::KV;
+    float *kmul = reinterpret_cast<float *>(aux + C::KMUL), *ve = reinterpret_cast<float *>(aux + C::VE),
+          *vinv = reinterpret_cast<float *>(aux + C::VINV), *sfac = reinterpret_cast<float *>(aux + C::FAC);
+    uint32_t *flags = reinterpret_cast<uint32_t *>(aux + C::FLAGS);  // [kInfo][4 groups of 32 keys](holes, slow)
+    float2 *sml = reinterpret_cast<float2 *>(aux + C::ML);
+    __shared__ uint64_t kfull[2], vfull[2], kempty[2], vempty[2], sfull[2], pready[2], pvdone, odone;
+    __shared__ uint32_t tmem_base;
+    __shared__ int s_abort, s_b;
+    __shared__ int64_t s_sum[kThreads / 32], s_before;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    griddep_launch_dependents();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kfull[i], 4);
+            mbar_init(&vfull[i], 4);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vempty[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pready[i], 4);
+        }
+        mbar_init(&pvdone, 1);
+        mbar_init(&odone, 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+
+    // ---- this CTA's run of units, and the item that it starts in
+    int64_t run = 0, inc = 0, v = 0;
+    auto scan = [&](int b0) {  // inc: units up to and with sequence b0 + threadIdx.x; run: with the whole chunk
+        const int b = b0 + threadIdx.x;
+        v = 0;
+        SeqBase s{0, 0, 0};
+        if (b < a.d.n_seqs) load_seq(s, a, b);
+        const int count = item_count(a, s.n, C::ROWS);
+        for (int rt = 0; rt < count && count <= 4; ++rt) v += item_units(item_of<D>(a, s, rt));
+        for (uint32_t many = __ballot_sync(kFullMask, count > 4); many; many &= many - 1) {
+            const int src = __ffs(many) - 1;  // long prompts: the whole warp
+            const SeqBase o{0, __shfl_sync(kFullMask, s.n, src), __shfl_sync(kFullMask, s.L, src)};
+            const int64_t sum = head_units<D>(a, o, lane);
+            if (lane == src) v = sum;
+        }
+        v *= a.c.n_kv_heads;
+        inc = v;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(kFullMask, inc, x);
+            if (lane >= x) inc += o;
+        }
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        inc += run;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int64_t o = s_sum[w];
+            if (w < warp) inc += o;
+            run += o;
+        }
+        __syncthreads();
+    };
+    for (int b0 = 0; b0 < a.d.n_seqs; b0 += kThreads) scan(b0);
+    const int64_t total = run;
+    const int ctas = (int)min(total, (int64_t)kSms);  // a unit each at least
+    Span *spans = static_cast<Span *>(a.workspace);
+    float *parts = reinterpret_cast<float *>(spans + kSplitMaxCtas);
+    if (threadIdx.x == 0) spans[blockIdx.x].parts = 0;
+    if (blockIdx.x >= ctas) return;
+    const int64_t u_lo = run_start(total, blockIdx.x, ctas), u_hi = run_start(total, blockIdx.x + 1, ctas);
+    {
+        int b0 = 0;
+        if (a.d.n_seqs > kThreads) {
+            run = 0;
+            for (b0 = -kThreads; run <= u_lo;) scan(b0 += kThreads);
+        }
+        if (inc - v <= u_lo && u_lo < inc) {
+            s_b = b0 + threadIdx.x;
+            s_before = inc - v;
+        }
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = tmem_base;
+
+    int b = uniform(s_b), hk = 0, rt = 0, first;  // units count from u_lo; first: of the item
+    SeqBase s;
+    load_seq(s, a, b);
+    Item it;
+    {
+        const int64_t per = head_units<D>(a, s, lane);
+        hk = uniform((int)((u_lo - s_before) / per));
+        int64_t rem = u_lo - s_before - hk * per;
+        for (;; rt += 32) {  // the item that holds unit `rem`
+            const int n = rt + lane < item_count(a, s.n, C::ROWS) ? item_units(item_of<D>(a, s, rt + lane)) : 0;
+            int64_t upto = n;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int64_t o = __shfl_up_sync(kFullMask, upto, x);
+                if (lane >= x) upto += o;
+            }
+            const uint32_t past = __ballot_sync(kFullMask, upto > rem);
+            if (past) {
+                const int src = __ffs(past) - 1;
+                rt += src;
+                first = -(int)(rem - __shfl_sync(kFullMask, upto - n, src));
+                break;
+            }
+            rem -= __shfl_sync(kFullMask, upto, 31);
+        }
+        it = item_of<D>(a, s, rt);
+    }
+    const int units = (int)(u_hi - u_lo);
+    const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)0x80000000);
+    uint32_t tc = 0;              // key tiles before this piece: buffers and phases
+    uint32_t sc[2] = {0, 0};      // steps before this piece in each S
+    uint32_t pvc = 0, pieces = 0;
+
+    for (int u = 0; u < units;) {
+        const int per = item_units(it);
+        const int u_end = min(first + per, units);
+        const bool whole = u == first && u_end == first + per;
+        const int kt0 = it.tile0 + (u - first);
+        const int nt = min(u_end - u, it.tile0 + it.tiles - kt0);  // 0: rows without keys
+        const bool dual = SLOTS == 2 && it.rows <= 128;
+        const int steps = SLOTS == 2 && !dual ? 2 * nt : nt;
+        const int p_first = s.L - s.n;
+
+        // ---- query rows: rotary, transform, fp16 with a power-of-two scale
+        const int q_rows = dual || SLOTS == 1 ? 128 : 256;
+        for (int r = warp; r < q_rows; r += 17) {
+            float q[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) q[i] = 0.f;
+            if (r < it.rows) {
+                const int i = (it.row0 + r) / a.group, h = hk * a.group + (it.row0 + r) - i * a.group;
+                const int64_t tok = s.t0 + i;
+                load_query_row<D>(q, a.q + tok * a.d.q_token_stride + (int64_t)h * D, tab,
+                                  tab.rd ? a.positions[tok] : 0, a.scale_log2 < 0.f ? -1.f : 1.f, lane);
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(q[i]));
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
+            const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 252u);
+            const float mul = m > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int d = lane * P + i;
+                *reinterpret_cast<__half *>(sq + (r >> 7) * C::Q + sw_chunk(128, r & 127, d >> 3) + place_of(d & 7) * 2) =
+                    __float2half_rn(q[i] * mul);
+            }
+            // above zero, so that a masked score stays -inf
+            if (lane == 0) sfac[r] = fmaxf(fabsf(a.scale_log2) * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+
+        // step n: key tile tile_of(n) of the piece, S n & 1
+        auto tile_of = [&](int n) { return SLOTS == 2 && !dual ? n >> 1 : n; };
+        if (warp == kMmaWarp) {
+            // ------------------------------------------------ matrix products
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = umma_idesc_f16(128, TK), idesc_o = umma_idesc_f16(128, D) | (1u << 16);
+                bool ok = true;
+                uint32_t s_n[2] = {sc[0], sc[1]};
+                auto product_s = [&](int n) {
+                    const uint32_t c = tc + tile_of(n), i = n & 1;
+                    if (!mbar_wait(&kfull[c & 1], (c >> 1) & 1, nullptr, &s_abort)) return false;
+                    tc_fence_after();
+                    const uint64_t qd = umma_desc_sw128(sq + (SLOTS == 2 && !dual ? i : 0) * C::Q);
+                    const uint64_t kd = umma_desc_sw128(sk + (c & 1) * C::KV);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        umma_f16(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
+                                 kd + (k >> 2) * (TK * 128 / 16) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
+                    umma_commit(&sfull[i]);
+                    if (SLOTS == 1 || dual || i) umma_commit(&kempty[c & 1]);
+                    return true;
+                };
+                for (int n = 0; n < 2 && n < steps && ok; ++n) ok = product_s(n);
+                for (int n = 0; n < steps && ok; ++n) {
+                    const uint32_t c = tc + tile_of(n), i = n & 1;
+                    ok = mbar_wait(&vfull[c & 1], (c >> 1) & 1, nullptr, &s_abort) &&
+                         mbar_wait(&pready[i], s_n[i] & 1, nullptr, &s_abort);
+                    if (!ok) break;
+                    ++s_n[i];
+                    tc_fence_after();
+                    const uint64_t vd = umma_desc_sw128_mn(sv + (c & 1) * C::KV, TK * 128);
+                    const bool fresh = SLOTS == 2 ? n < 2 : n == 0;
+#pragma unroll
+                    for (int k = 0; k < TK / 16; ++k)
+                        umma_ts(tbase + C::O_COL + (SLOTS == 2 ? i * D : 0), tbase + i * C::S_STEP + k * 8,
+                                vd + k * (2048 / 16), idesc_o, fresh && k == 0 ? 0u : 1u);
+                    if (SLOTS == 1) umma_commit(&pvdone);
+                    if (SLOTS == 1 || dual || i) umma_commit(&vempty[c & 1]);
+                    if (n + 2 < steps) ok = product_s(n + 2);
+                }
+                umma_commit(&odone);
+                mbar_wait(&odone, pieces & 1, nullptr, nullptr);  // before anything is torn down
+            }
+            __syncwarp();
+        } else if (warp >= 8) {
+            // ------------------------------------------------ expanding keys (warps 8-11) and values (12-15)
+            const bool is_v = warp >= 12;
+            const int id = threadIdx.x - (is_v ? 384 : 256), row = id % TK, part = id / TK;
+            const int32_t *table = a.table + (int64_t)b * a.d.max_pages;
+            const uint8_t *codes = static_cast<const uint8_t *>(is_v ? a.c.v_codes : a.c.k_codes) + part * (C::NW * 16);
+            const uint8_t *vsc = static_cast<const uint8_t *>(a.c.v_scales), *ksc = static_cast<const uint8_t *>(a.c.k_scales);
+            uint32_t page = ~0u;
+            auto find = [&](int jj) {  // the page of this thread's key in tile jj
+                const int64_t key = (int64_t)(kt0 + jj) * TK + row;
+                page = jj < nt && key < s.L ? (uint32_t)__ldg(table + (key >> a.page_shift)) : ~0u;
+            };
+            uint4 w[C::NW];
+            uint32_t vs[NB / 2], ks[NB / 2];
+            bool here = false;
+            auto load = [&](int jj) {
+                here = page < n_pages;
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) vs[i] = ks[i] = 0u;
+#pragma unroll
+                for (int i = 0; i < C::NW; ++i) w[i] = make_uint4(0, 0, 0, 0);
+                if (here) {
+                    const int slot = (int)(((int64_t)(kt0 + jj) * TK + row) & (a.c.page_size - 1));
+                    const uint64_t at = ((page * a.c.n_kv_heads + hk) << a.page_shift) + (uint32_t)slot;
+#pragma unroll
+                    for (int i = 0; i < C::NW; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + at * (D / 2)) + i);
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) {
+                        vs[i] = __ldg(reinterpret_cast<const uint32_t *>(vsc + at * (D / 16)) + i);
+                        if (!is_v) ks[i] = __ldg(reinterpret_cast<const uint32_t *>(ksc + at * (D / 16)) + i);
+                    }
+                }
+            };
+            find(0);
+            load(0);
+            find(1);
+            for (int jj = 0; jj < nt; ++jj) {
+                const uint32_t c = tc + jj;
+                // the scales' ranges decide for 32 keys at a time; keys and values see the same numbers
+                auto range = [&](const uint32_t (&x)[NB / 2], uint32_t &top) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) m = max(m, max(x[i] << 17, (x[i] & 0x7fff0000u) << 1));
+                    top = m >> 17;
+                    return __any_sync(kFullMask, m >= 0x6c00u << 17) || !__any_sync(kFullMask, m >= 0x1400u << 17);
+                };
+                uint32_t vtop, ktop = 0;
+                const bool v_slow = range(vs, vtop), k_slow = !is_v && range(ks, ktop);
+                const int ev = (int)max(vtop >> 10, 1u) - 16, ek = (int)max(ktop >> 10, 1u) - 16;  // s 2^-e in [2, 4)
+                if (!is_v && part == 0) {
+                    const int info = c & (kInfo - 1);
+                    const uint32_t holes = __ballot_sync(kFullMask, !here && (int64_t)(kt0 + jj) * TK + row < s.L);
+                    if (lane == 0) {
+                        flags[info * 8 + (row >> 5) * 2] = holes;
+                        flags[info * 8 + (row >> 5) * 2 + 1] = (k_slow ? 1u : 0u) | (v_slow ? 2u : 0u);
+                    }
+                    if (k_slow || v_slow) {
+                        kmul[info * TK + row] = k_slow ? __int_as_float((127 + ek) << 23) : 1.f;
+                        ve[info * TK + row] = v_slow ? (float)ev : 0.f;
+                        vinv[info * TK + row] = v_slow ? __int_as_float((127 - ev) << 23) : 1.f;
+                    }
+                }
+                const bool slow = is_v ? v_slow : k_slow;
+                const int e = is_v ? ev : ek;
+                uint4 cw[C::NW];
+                uint32_t cs[C::NW];
+#pragma unroll
+                for (int i = 0; i < C::NW; ++i) {
+                    cw[i] = w[i];
+                    const int k = part * C::NW + i;
+                    const uint32_t x = is_v ? (NB > 4 ? (part ? vs[2 + i / 2] : vs[i / 2]) : vs[i / 2])
+                                            : (NB > 4 ? (part ? ks[2 + i / 2] : ks[i / 2]) : ks[i / 2]);
+                    cs[i] = __byte_perm(x, 0, (k & 1) ? 0x3232 : 0x1010);
+                }
+                load(jj + 1);
+                find(jj + 2);
+                uint64_t *full = is_v ? &vfull[c & 1] : &kfull[c & 1], *empty = is_v ? &vempty[c & 1] : &kempty[c & 1];
+                if (!mbar_wait(empty, ((c >> 1) & 1) ^ 1, nullptr, &s_abort)) break;
+                uint8_t *to = (is_v ? sv : sk) + (c & 1) * C::KV;
+                if (slow) {
+                    const __half2 mul = bits_h2((uint32_t)(15 - e) * 0x04000400u);  // 2^-e, -15 <= e <= 14
+#pragma unroll
+                    for (int i = 0; i < C::NW; ++i) cs[i] = h2_bits(__hmul2(bits_h2(cs[i]), mul));
+                }
+                const __half2 off = __floats2half2_rn(-1032.f, -1032.f), off64 = __floats2half2_rn(-72.f, -72.f);
+#pragma unroll
+                for (int i = 0; i < C::NW; ++i) {
+                    const uint32_t words[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
+                    const __half2 sc2 = bits_h2(cs[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t x = words[j], y = x >> 8;
+                        uint4 o;
+                        o.x = h2_bits(__hmul2(__hadd2(bits_h2(and_or(x, 0x000f000fu, 0x64006400u)), off), sc2));
+                        o.y = h2_bits(__hmul2(__hadd2(bits_h2(and_or(x, 0x00f000f0u, 0x54005400u)), off64), sc2));
+                        o.z = h2_bits(__hmul2(__hadd2(bits_h2(and_or(y, 0x000f000fu, 0x64006400u)), off), sc2));
+                        o.w = h2_bits(__hmul2(__hadd2(bits_h2(and_or(y, 0x00f000f0u, 0x54005400u)), off64), sc2));
+                        *reinterpret_cast<uint4 *>(to + sw_chunk(TK, row, (part * C::NW + i) * 4 + j)) = o;
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            }
+        } else {
+            // ------------------------------------------------ softmax: S slot (warps 0-3, 4-7), a thread per row
+            const int slot = warp >> 2, tr = threadIdx.x & 127;
+            const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t ocol = lanes + C::O_COL + (SLOTS == 2 ? slot * D : 0);
+            const int r = (SLOTS == 2 && !dual ? slot * 128 : 0) + tr;  // of the item
+            const int p = p_first + (it.row0 + min(r, it.rows - 1)) / a.group;
+            const int hi = min(p, s.L - 1), lo = a.d.window > 0 ? (int)max((int64_t)p - a.d.window, (int64_t)-1) : -1;
+            const int full_hi = p_first + it.row0 / a.group;
+            const int full_lo =
+                a.d.window > 0 ? (int)max((int64_t)p_first + (it.row0 + it.rows - 1) / a.group - a.d.window, (int64_t)-1) : -1;
+            const float fac = sfac[r];
+            float M = -FLT_MAX, l = 0.f;
+            uint32_t n_s[2] = {sc[0], sc[1]};
+            bool ok = true;
+            int mine = 0;  // steps of this slot
+            for (int n = slot; n < steps && slot < SLOTS; n += SLOTS, ++mine) {
+                const int i = SLOTS == 2 ? slot : n & 1;
+                const int jj = tile_of(n), k0 = (kt0 + jj) * TK, info = (tc + jj) & (kInfo - 1);
+                ok = mbar_wait(&sfull[i], n_s[i] & 1, nullptr, &s_abort);
+                if (!ok) break;
+                ++n_s[i];
+                tc_fence_after();
+                const uint32_t scol = lanes + i * C::S_STEP;
+                uint32_t holes[TK / 32], slow = 0, any = 0;
+#pragma unroll
+                for (int g = 0; g < TK / 32; ++g) {
+                    const uint2 f = *reinterpret_cast<const uint2 *>(flags + info * 8 + g * 2);
+                    holes[g] = f.x;
+                    any |= f.x;
+                    slow |= f.y;
+                }
+                const bool plain = k0 + TK - 1 <= full_hi && k0 > full_lo && any == 0;
+                auto masked = [&](float (&x)[32], int g) {
+                    const int c0 = k0 + 32 * g;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c0 + e > hi || c0 + e <= lo || (holes[g] >> e & 1)) x[e] = -INFINITY;
+                };
+                const bool has_slow = slow != 0;
+                auto is_slow = [&](int g) { return has_slow && flags[info * 8 + g * 2 + 1] != 0; };
+                auto fetch = [&](float (&x)[32], int g) {
+                    tmem_ld32(scol + 32 * g, x);
+                    tmem_ld_wait();
+                    if (is_slow(g))  // these come out in the unit of M, the others in that of 1 / fac
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = fmaf(x[e] * kmul[info * TK + 32 * g + e], fac, ve[info * TK + 32 * g + e]);
+                    if (!plain) masked(x, g);
+                };
+                float top = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < TK / 32; ++g) {
+                    float x[32];
+                    fetch(x, g);
+                    float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+#pragma unroll
+                    for (int e = 4; e < 32; e += 4) {
+                        t0 = fmaxf(t0, x[e]);
+                        t1 = fmaxf(t1, x[e + 1]);
+                        t2 = fmaxf(t2, x[e + 2]);
+                        t3 = fmaxf(t3, x[e + 3]);
+                    }
+                    top = fmaxf(top, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * (is_slow(g) ? 1.f : fac));
+                }
+                if (__any_sync(kFullMask, top > M + 11.f)) {
+                    const float m = fmaxf(M, top - 6.f), f = ex2(M - m);
+                    if (SLOTS == 1 && n > 0) {  // the last product may still run: S of this step was issued before it
+                        ok = mbar_wait(&pvdone, (pvc + n - 1) & 1, nullptr, &s_abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    M = m;
+                    l *= f;
+                    if (mine) {
+#pragma unroll 1
+                        for (int g = 0; g < D / 16; ++g) {
+                            float x[16];
+                            uint32_t y[16];
+                            tmem_ld16(ocol + 16 * g, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * f);
+                            tmem_st16(ocol + 16 * g, y);
+                        }
+                    }
+                }
+                const uint64_t m2 = pack2(-M, -M);
+                uint64_t sum = pack2(0.f, 0.f);
+#pragma unroll
+                for (int g = 0; g < TK / 32; ++g) {
+                    float x[32];
+                    fetch(x, g);
+                    const float fg = is_slow(g) ? 1.f : fac;
+                    const uint64_t f2 = pack2(fg, fg);
+                    uint32_t y[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 z = unpack2(fma2(pack2(x[e], x[e + 1]), f2, m2));
+                        x[e] = ex2(z.x), x[e + 1] = ex2(z.y);
+                        y[e / 2] = h2_bits(__floats2half2_rn(x[e], x[e + 1]));
+                    }
+                    if (is_slow(g)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] *= vinv[info * TK + 32 * g + e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) sum = add2(sum, pack2(x[e], x[e + 1]));
+                    tmem_st16(scol + 16 * g, y);
+                }
+                const float2 z = unpack2(sum);
+                l += z.x + z.y;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pready[i]);
+            }
+            // ---- the rows' results
+            if (slot < SLOTS) {
+                ok = mbar_wait(&odone, pieces & 1, nullptr, &s_abort) && ok;
+                tc_fence_after();
+                float *other = reinterpret_cast<float *>(sk);  // the second O of a dual item: [D][128 rows]
+                float f0 = 1.f, f1 = 0.f;
+                if (dual) {
+                    if (slot == 1) {
+                        sml[tr] = make_float2(M, mine ? l : 0.f);
+#pragma unroll 1
+                        for (int g = 0; g < D / 16 && mine; ++g) {
+                            float x[16];
+                            tmem_ld16(ocol + 16 * g, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) other[(16 * g + e) * 128 + tr] = x[e];
+                        }
+                    }
+                    named_barrier(1, 256);
+                    const float2 y = sml[tr];
+                    const float m = fmaxf(M, y.x);
+                    f0 = ex2(M - m), f1 = nt > 1 ? ex2(y.x - m) : 0.f;
+                    l = l * f0 + y.y * f1;
+                    M = m;
+                }
+                // all lanes of a warp read tensor memory together
+                const bool store = (!dual || slot == 0) && r < it.rows;
+                // a broken wait must not pass for a result
+                const float bad = ok && !*(volatile int *)&s_abort ? 1.f : NAN;
+                const float norm = whole ? bad * (l > 0.f ? rsqrt_dim<D>() / l : 0.f) : bad;
+                f0 *= norm, f1 *= norm;
+                if (!dual || slot == 0) {
+                    auto row16 = [&](float (&x)[16], int col) {  // 16 columns, values in order
+                        float y[16];
+                        tmem_ld16(ocol + col, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float z = mine ? y[e] * f0 : 0.f;
+                            if (dual && nt > 1) z = fmaf(other[(col + e) * 128 + tr], f1, z);
+                            x[(e & 8) + value_at(e & 7)] = z;
+                        }
+                    };
+                    if (whole) {
+                        const int i = (it.row0 + r) / a.group, h = hk * a.group + it.row0 + r - i * a.group;
+                        __nv_bfloat16 *dst = a.out + (s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
+                        // H of D = H of D / 64 over H of 64: one 64-value output block at a time
+#pragma unroll 1
+                        for (int q = 0; q < D / 64; ++q) {
+                            float x[64];
+#pragma unroll
+                            for (int j = 0; j < D / 64; ++j) {
+                                const float sg = __popc(j & q) & 1 ? -1.f : 1.f;
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    float y[16];
+                                    row16(y, 64 * j + 16 * g);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) x[16 * g + e] = j ? fmaf(sg, y[e], x[16 * g + e]) : y[e];
+                                }
+                            }
+#pragma unroll
+                            for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+                                for (int e = 0; e < 64; ++e)
+                                    if (!(e & d)) {
+                                        const float y = x[e], z = x[e + d];
+                                        x[e] = y + z;
+                                        x[e + d] = y - z;
+                                    }
+                            if (store) {
+#pragma unroll
+                                for (int e = 0; e < 64; e += 8)
+                                    *reinterpret_cast<uint4 *>(dst + 64 * q + e) =
+                                        make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
+                                                   pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
+                            }
+                        }
+                    } else {
+                        float *part = parts + (int64_t)((blockIdx.x * 2 + (u ? 1 : 0)) * C::ROWS + r) * C::PART;
+#pragma unroll 1
+                        for (int g = 0; g < D / 16; ++g) {
+                            float x[16];
+                            row16(x, 16 * g);
+                            if (store)
+#pragma unroll
+                                for (int e = 0; e < 16; e += 4)
+                                    *reinterpret_cast<float4 *>(part + 16 * g + e) =
+                                        make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        }
+                        if (store) part[D] = M, part[D + 1] = l;
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+
+        // ---- the next piece
+        if (u == first && !whole && threadIdx.x == 0) {
+            // it starts here and ends in the CTA that holds its last unit
+            const int64_t last = u_lo + first + per - 1;
+            int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
+            while (run_start(total, c + 1, ctas) <= last) ++c;
+            spans[blockIdx.x] = Span{c - (int)blockIdx.x + 1, u ? 1 : 0, (int)s.t0, it.rows, hk, it.row0, {0, 0}};
+        }
+        tc += nt;
+        if (SLOTS == 2)
+            sc[0] += dual ? (nt + 1) / 2 : nt, sc[1] += dual ? nt / 2 : nt;
+        else
+            sc[0] += (nt + 1) / 2, sc[1] += nt / 2, pvc += nt;
+        ++pieces;
+        u = u_end;
+        if (u < units) {
+            first += per;
+            if (++rt == item_count(a, s.n, C::ROWS)) {
+                rt = 0;
+                if (++hk == a.c.n_kv_heads) {
+                    hk = 0;
+                    do {
+                        load_seq(s, a, ++b);
+                    } while (s.n == 0);
+                }
+            }
+            it = item_of<D>(a, s, rt);
+        }
+        __syncthreads();
+        if (*(volatile int *)&s_abort) break;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
+    using C = Tiles<D>;
+    const cudaError_t e = cudaFuncSetAttribute(k_attn_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    k_attn_tiles<D><<<kSms, kThreads, C::SMEM, st>>>(tab, a);
+    return launch_join<D, C::ROWS>(a, kSms, st);
+}
+
+}  // namespace
+
+size_t attn_tiles_part_bytes(int head_dim) {
+    const size_t rows = head_dim == 256 ? Tiles<256>::ROWS : Tiles<128>::ROWS;
+    return 2 * rows * kSms * sizeof(float) * (head_dim + 4);
+}
+
+cudaError_t launch_attn_tiles(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
+    if (a.c.head_dim == 64) return launch<64>(tab, a, st);
+    if (a.c.head_dim == 128) return launch<128>(tab, a, st);
+    return launch<256>(tab, a, st);
+}
+
+}  // namespace strata
