@@ -638,7 +638,7 @@ cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t s
     const cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     k_attn_split<D, NT><<<C::CTAS, kSplitWarps * 32, C::SMEM, st>>>(tab, a);
-    return launch_join<D, C::ROWS>(a, C::CTAS, st);
+    return launch_join<D, C::ROWS, 8>(a, C::CTAS, st);
 }
 
 }  // namespace

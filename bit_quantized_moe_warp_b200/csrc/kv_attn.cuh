@@ -76,19 +76,21 @@ struct Span {  // what k_attn_join needs of the last piece of a CTA
     int pad[2];
 };
 
-// One block for each piece that several CTAs share and two of its query rows:
-// eight warps over the parts of a row, then over each other, in a fixed order.
-template <int D, int ROWS>
+// One block for each piece that several CTAs share and 16 / WPR of its query
+// rows at a time: WPR warps over the parts of a row, then over each other, in a
+// fixed order. Few rows of many parts take 8 warps, many rows of few parts 1.
+template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
     constexpr int P = D / 32, PART = D + 4;
-    __shared__ float so[8][2][D], sl[8][2], sw[2][kSplitMaxCtas];
+    constexpr int RPB = 16 / WPR;
+    __shared__ float so[WPR][RPB][D], sl[WPR][RPB], sw[RPB][kSplitMaxCtas];
     griddep_wait();
     const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
     if (sp.parts == 0) return;
     const float *parts = reinterpret_cast<const float *>(static_cast<const Span *>(a.workspace) + kSplitMaxCtas);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wr = warp & 1, wq = warp >> 1;
-    for (int r0 = 2 * blockIdx.y; r0 < sp.rows; r0 += 2 * gridDim.y) {
+    const int wr = warp % RPB, wq = warp / RPB;
+    for (int r0 = RPB * blockIdx.y; r0 < sp.rows; r0 += RPB * gridDim.y) {
         const int r = r0 + wr;
         const bool live = r < sp.rows;
         auto at = [&](int i) {
@@ -103,14 +105,14 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
 #pragma unroll
         for (int j = 0; j < P; ++j) v[j] = 0.f;
         if (live) {
-            for (int i = wq + 8 * lane; i < sp.parts; i += 256) {  // the parts of this warp
+            for (int i = wq + WPR * lane; i < sp.parts; i += 32 * WPR) {  // the parts of this warp
                 const float f = ex2(at(i)[D] - m);
                 sw[wr][i] = f;
                 sum = fmaf(at(i)[D + 1], f, sum);
             }
             __syncwarp();
 #pragma unroll 4
-            for (int i = wq; i < sp.parts; i += 8) {
+            for (int i = wq; i < sp.parts; i += WPR) {
                 const float f = sw[wr][i];
                 float w[P];
                 if constexpr (P == 2) *reinterpret_cast<float2 *>(w) = *reinterpret_cast<const float2 *>(at(i) + lane * P);
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
         __syncthreads();
         if (wq == 0 && live) {
 #pragma unroll
-            for (int w = 1; w < 8; ++w) {
+            for (int w = 1; w < WPR; ++w) {
                 sum += sl[w][wr];
 #pragma unroll
                 for (int j = 0; j < P; ++j) v[j] += so[w][wr][lane * P + j];
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
     }
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, int WPR>
 cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
     // programmatic launch: the blocks come up while the last CTAs finish
     cudaLaunchAttribute attr = {};
@@ -149,12 +151,13 @@ cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     const int64_t rows = (int64_t)a.d.max_q_len * a.group;  // a hint only: a block takes more rows in turn
-    cfg.gridDim = dim3(ctas, rows < 2 ? 1 : rows < ROWS ? (unsigned)(rows + 1) / 2 : ROWS / 2);
+    constexpr int RPB = 16 / WPR;
+    cfg.gridDim = dim3(ctas, rows < 1 ? 1 : rows < ROWS ? (unsigned)(rows + RPB - 1) / RPB : ROWS / RPB);
     cfg.blockDim = dim3(512);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<D, ROWS>, a);
+    return cudaLaunchKernelEx(&cfg, k_attn_join<D, ROWS, WPR>, a);
 }
 
 // Many query rows (kv_attn_tiles.cu): bytes of its partial results, and the launch

@@ -26,12 +26,14 @@
 //
 // Work: the key tiles of all items in a row, cut into 148 equal runs, one for
 // each CTA; pieces of an item that several CTAs share go through k_attn_join.
+#include <type_traits>
+
 #include "kv_attn.cuh"
 
 namespace strata {
 namespace {
 
-constexpr int kThreads = 17 * 32;
+constexpr int kThreads = 20 * 32;  // the last three warps only complete a group of four
 constexpr int kMmaWarp = 16;
 constexpr int kInfo = 4;  // tiles whose flags are kept
 
@@ -96,6 +98,13 @@ STRATA_DEV uint64_t umma_desc_sw128_mn(const void *tile, uint32_t block) {
     return ((a >> 4) & 0x3FFFull) | ((uint64_t)(block >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// Registers of a group of four warps. 640 threads at 96 each are 480 for every
+// four-warp column; afterwards 2 x 128 + 2 x 80 + 64 = 480.
+template <int N>
+STRATA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+STRATA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 STRATA_DEV uint64_t pack2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -149,6 +158,16 @@ STRATA_DEV Item item_of(const AttnArgs &a, const SeqBase &s, int rt) {
 }
 // units of an item; one at least, which writes the zeros of rows without keys
 STRATA_DEV int item_units(const Item &it) { return max(it.tiles, 1); }
+
+// A run of a CTA's key tiles inside one item, and what came before it
+struct Piece {
+    int b, hk, rt, first, u, u_end;  // units count from the CTA's first; first: of the item
+    SeqBase s;
+    Item it;
+    int kt0, nt, steps;
+    bool whole, dual;
+    uint32_t tc, sc[2], count;  // key tiles, steps in each S, pieces so far: buffers and phases
+};
 
 STRATA_DEV int item_count(const AttnArgs &a, int n, int rows) { return (int)(((int64_t)n * a.group + rows - 1) / rows); }
 
@@ -286,29 +305,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int units = (int)(u_hi - u_lo);
     const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)0x80000000);
-    uint32_t tc = 0;              // key tiles before this piece: buffers and phases
-    uint32_t sc[2] = {0, 0};      // steps before this piece in each S
-    uint32_t pvc = 0, pieces = 0;
 
-    for (int u = 0; u < units;) {
-        const int per = item_units(it);
-        const int u_end = min(first + per, units);
-        const bool whole = u == first && u_end == first + per;
-        const int kt0 = it.tile0 + (u - first);
-        const int nt = min(u_end - u, it.tile0 + it.tiles - kt0);  // 0: rows without keys
-        const bool dual = SLOTS == 2 && it.rows <= 128;
-        const int steps = SLOTS == 2 && !dual ? 2 * nt : nt;
-        const int p_first = s.L - s.n;
+    // Every role walks over the pieces by itself, with its own registers.
+    // load_q: the warps that bring the query rows.
+    auto pieces = [&](auto load_q, auto &&role) {
+    Piece p{};
+    p.b = b, p.hk = hk, p.rt = rt, p.first = first, p.s = s, p.it = it;
+    for (; p.u < units;) {
+        const int per = item_units(p.it);
+        p.u_end = min(p.first + per, units);
+        p.whole = p.u == p.first && p.u_end == p.first + per;
+        p.kt0 = p.it.tile0 + (p.u - p.first);
+        p.nt = min(p.u_end - p.u, p.it.tile0 + p.it.tiles - p.kt0);  // 0: rows without keys
+        p.dual = SLOTS == 2 && p.it.rows <= 128;
+        p.steps = SLOTS == 2 && !p.dual ? 2 * p.nt : p.nt;
 
+        if constexpr (decltype(load_q)::value) {
         // ---- query rows: rotary, transform, fp16 with a power-of-two scale
-        const int q_rows = dual || SLOTS == 1 ? 128 : 256;
-        for (int r = warp; r < q_rows; r += 17) {
+        const int q_rows = p.dual || SLOTS == 1 ? 128 : 256;
+        for (int r = warp; r < q_rows; r += kMmaWarp) {
             float q[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) q[i] = 0.f;
-            if (r < it.rows) {
-                const int i = (it.row0 + r) / a.group, h = hk * a.group + (it.row0 + r) - i * a.group;
-                const int64_t tok = s.t0 + i;
+            if (r < p.it.rows) {
+                const int i = (p.it.row0 + r) / a.group, h = p.hk * a.group + (p.it.row0 + r) - i * a.group;
+                const int64_t tok = p.s.t0 + i;
                 load_query_row<D>(q, a.q + tok * a.d.q_token_stride + (int64_t)h * D, tab,
                                   tab.rd ? a.positions[tok] : 0, a.scale_log2 < 0.f ? -1.f : 1.f, lane);
             }
@@ -329,35 +350,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) sfac[r] = fmaxf(fabsf(a.scale_log2) * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
         }
         fence_proxy_async_smem();
+        }
         tc_fence_before();
-        __syncthreads();
+        named_barrier(0, kThreads);
         tc_fence_after();
 
-        // step n: key tile tile_of(n) of the piece, S n & 1
-        auto tile_of = [&](int n) { return SLOTS == 2 && !dual ? n >> 1 : n; };
-        if (warp == kMmaWarp) {
+        role(p);
+        // ---- the next piece
+        if (p.u == p.first && !p.whole && threadIdx.x == 0) {
+            // it starts here and ends in the CTA that holds its last unit
+            const int64_t last = u_lo + p.first + per - 1;
+            int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
+            while (run_start(total, c + 1, ctas) <= last) ++c;
+            spans[blockIdx.x] = Span{c - (int)blockIdx.x + 1, p.u ? 1 : 0, (int)p.s.t0, p.it.rows, p.hk, p.it.row0, {0, 0}};
+        }
+        p.tc += p.nt;
+        if (SLOTS == 2)
+            p.sc[0] += p.dual ? (p.nt + 1) / 2 : p.nt, p.sc[1] += p.dual ? p.nt / 2 : p.nt;
+        else
+            p.sc[0] += (p.nt + 1) / 2, p.sc[1] += p.nt / 2;
+        ++p.count;
+        p.u = p.u_end;
+        if (p.u < units) {
+            p.first += per;
+            if (++p.rt == item_count(a, p.s.n, C::ROWS)) {
+                p.rt = 0;
+                if (++p.hk == a.c.n_kv_heads) {
+                    p.hk = 0;
+                    do {
+                        load_seq(p.s, a, ++p.b);
+                    } while (p.s.n == 0);
+                }
+            }
+            p.it = item_of<D>(a, p.s, p.rt);
+        }
+        tc_fence_before();
+        named_barrier(0, kThreads);
+        tc_fence_after();
+        if (*(volatile int *)&s_abort) break;
+    }
+    };
+
+    if (warp >= kMmaWarp) {
+        regs_down<64>();
+        pieces(std::false_type{}, [&](const Piece &p) {
+        auto tile_of = [&](int n) { return SLOTS == 2 && !p.dual ? n >> 1 : n; };  // of step n, in S n & 1
             // ------------------------------------------------ matrix products
-            if (lane == 0) {
+            if (warp == kMmaWarp && lane == 0) {
                 constexpr uint32_t idesc_s = umma_idesc_f16(128, TK), idesc_o = umma_idesc_f16(128, D) | (1u << 16);
                 bool ok = true;
-                uint32_t s_n[2] = {sc[0], sc[1]};
+                uint32_t s_n[2] = {p.sc[0], p.sc[1]};
                 auto product_s = [&](int n) {
-                    const uint32_t c = tc + tile_of(n), i = n & 1;
+                    const uint32_t c = p.tc + tile_of(n), i = n & 1;
                     if (!mbar_wait(&kfull[c & 1], (c >> 1) & 1, nullptr, &s_abort)) return false;
                     tc_fence_after();
-                    const uint64_t qd = umma_desc_sw128(sq + (SLOTS == 2 && !dual ? i : 0) * C::Q);
+                    const uint64_t qd = umma_desc_sw128(sq + (SLOTS == 2 && !p.dual ? i : 0) * C::Q);
                     const uint64_t kd = umma_desc_sw128(sk + (c & 1) * C::KV);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         umma_f16(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
                                  kd + (k >> 2) * (TK * 128 / 16) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
                     umma_commit(&sfull[i]);
-                    if (SLOTS == 1 || dual || i) umma_commit(&kempty[c & 1]);
+                    if (SLOTS == 1 || p.dual || i) umma_commit(&kempty[c & 1]);
                     return true;
                 };
-                for (int n = 0; n < 2 && n < steps && ok; ++n) ok = product_s(n);
-                for (int n = 0; n < steps && ok; ++n) {
-                    const uint32_t c = tc + tile_of(n), i = n & 1;
+                for (int n = 0; n < 2 && n < p.steps && ok; ++n) ok = product_s(n);
+                for (int n = 0; n < p.steps && ok; ++n) {
+                    const uint32_t c = p.tc + tile_of(n), i = n & 1;
                     ok = mbar_wait(&vfull[c & 1], (c >> 1) & 1, nullptr, &s_abort) &&
                          mbar_wait(&pready[i], s_n[i] & 1, nullptr, &s_abort);
                     if (!ok) break;
@@ -370,24 +429,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_ts(tbase + C::O_COL + (SLOTS == 2 ? i * D : 0), tbase + i * C::S_STEP + k * 8,
                                 vd + k * (2048 / 16), idesc_o, fresh && k == 0 ? 0u : 1u);
                     if (SLOTS == 1) umma_commit(&pvdone);
-                    if (SLOTS == 1 || dual || i) umma_commit(&vempty[c & 1]);
-                    if (n + 2 < steps) ok = product_s(n + 2);
+                    if (SLOTS == 1 || p.dual || i) umma_commit(&vempty[c & 1]);
+                    if (n + 2 < p.steps) ok = product_s(n + 2);
                 }
                 umma_commit(&odone);
-                mbar_wait(&odone, pieces & 1, nullptr, nullptr);  // before anything is torn down
+                mbar_wait(&odone, p.count & 1, nullptr, nullptr);  // before anything is torn down
             }
             __syncwarp();
-        } else if (warp >= 8) {
+        });
+    } else if (warp >= 8) {
+        regs_down<80>();
+        pieces(std::true_type{}, [&](const Piece &p) {
             // ------------------------------------------------ expanding keys (warps 8-11) and values (12-15)
             const bool is_v = warp >= 12;
             const int id = threadIdx.x - (is_v ? 384 : 256), row = id % TK, part = id / TK;
-            const int32_t *table = a.table + (int64_t)b * a.d.max_pages;
+            const int32_t *table = a.table + (int64_t)p.b * a.d.max_pages;
             const uint8_t *codes = static_cast<const uint8_t *>(is_v ? a.c.v_codes : a.c.k_codes) + part * (C::NW * 16);
             const uint8_t *vsc = static_cast<const uint8_t *>(a.c.v_scales), *ksc = static_cast<const uint8_t *>(a.c.k_scales);
             uint32_t page = ~0u;
             auto find = [&](int jj) {  // the page of this thread's key in tile jj
-                const int64_t key = (int64_t)(kt0 + jj) * TK + row;
-                page = jj < nt && key < s.L ? (uint32_t)__ldg(table + (key >> a.page_shift)) : ~0u;
+                const int64_t key = (int64_t)(p.kt0 + jj) * TK + row;
+                page = jj < p.nt && key < p.s.L ? (uint32_t)__ldg(table + (key >> a.page_shift)) : ~0u;
             };
             uint4 w[C::NW];
             uint32_t vs[NB / 2], ks[NB / 2];
@@ -399,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < C::NW; ++i) w[i] = make_uint4(0, 0, 0, 0);
                 if (here) {
-                    const int slot = (int)(((int64_t)(kt0 + jj) * TK + row) & (a.c.page_size - 1));
-                    const uint64_t at = ((page * a.c.n_kv_heads + hk) << a.page_shift) + (uint32_t)slot;
+                    const int slot = (int)(((int64_t)(p.kt0 + jj) * TK + row) & (a.c.page_size - 1));
+                    const uint64_t at = ((page * a.c.n_kv_heads + p.hk) << a.page_shift) + (uint32_t)slot;
 #pragma unroll
                     for (int i = 0; i < C::NW; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + at * (D / 2)) + i);
 #pragma unroll
@@ -413,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             find(0);
             load(0);
             find(1);
-            for (int jj = 0; jj < nt; ++jj) {
-                const uint32_t c = tc + jj;
+            for (int jj = 0; jj < p.nt; ++jj) {
+                const uint32_t c = p.tc + jj;
                 // the scales' ranges decide for 32 keys at a time; keys and values see the same numbers
                 auto range = [&](const uint32_t (&x)[NB / 2], uint32_t &top) {
                     uint32_t m = 0;
@@ -428,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int ev = (int)max(vtop >> 10, 1u) - 16, ek = (int)max(ktop >> 10, 1u) - 16;  // s 2^-e in [2, 4)
                 if (!is_v && part == 0) {
                     const int info = c & (kInfo - 1);
-                    const uint32_t holes = __ballot_sync(kFullMask, !here && (int64_t)(kt0 + jj) * TK + row < s.L);
+                    const uint32_t holes = __ballot_sync(kFullMask, !here && (int64_t)(p.kt0 + jj) * TK + row < p.s.L);
                     if (lane == 0) {
                         flags[info * 8 + (row >> 5) * 2] = holes;
                         flags[info * 8 + (row >> 5) * 2 + 1] = (k_slow ? 1u : 0u) | (v_slow ? 2u : 0u);
@@ -481,101 +543,103 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);
             }
-        } else {
+        });
+    } else {
+        regs_up<128>();
+        pieces(std::true_type{}, [&](const Piece &p) {
+        auto tile_of = [&](int n) { return SLOTS == 2 && !p.dual ? n >> 1 : n; };  // of step n, in S n & 1
             // ------------------------------------------------ softmax: S slot (warps 0-3, 4-7), a thread per row
             const int slot = warp >> 2, tr = threadIdx.x & 127;
             const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
             const uint32_t ocol = lanes + C::O_COL + (SLOTS == 2 ? slot * D : 0);
-            const int r = (SLOTS == 2 && !dual ? slot * 128 : 0) + tr;  // of the item
-            const int p = p_first + (it.row0 + min(r, it.rows - 1)) / a.group;
-            const int hi = min(p, s.L - 1), lo = a.d.window > 0 ? (int)max((int64_t)p - a.d.window, (int64_t)-1) : -1;
-            const int full_hi = p_first + it.row0 / a.group;
+            const int r = (SLOTS == 2 && !p.dual ? slot * 128 : 0) + tr;  // of the item
+            const int pos = p.s.L - p.s.n + (p.it.row0 + min(r, p.it.rows - 1)) / a.group;
+            const int hi = min(pos, p.s.L - 1), lo = a.d.window > 0 ? (int)max((int64_t)pos - a.d.window, (int64_t)-1) : -1;
+            const int full_hi = p.s.L - p.s.n + p.it.row0 / a.group;
             const int full_lo =
-                a.d.window > 0 ? (int)max((int64_t)p_first + (it.row0 + it.rows - 1) / a.group - a.d.window, (int64_t)-1) : -1;
+                a.d.window > 0 ? (int)max((int64_t)p.s.L - p.s.n + (p.it.row0 + p.it.rows - 1) / a.group - a.d.window, (int64_t)-1) : -1;
             const float fac = sfac[r];
             float M = -FLT_MAX, l = 0.f;
-            uint32_t n_s[2] = {sc[0], sc[1]};
+            uint32_t n_s[2] = {p.sc[0], p.sc[1]};
             bool ok = true;
-            int mine = 0;  // steps of this slot
-            for (int n = slot; n < steps && slot < SLOTS; n += SLOTS, ++mine) {
+            int mine = 0;  // p.steps of this slot
+            for (int n = slot; n < p.steps && slot < SLOTS; n += SLOTS, ++mine) {
                 const int i = SLOTS == 2 ? slot : n & 1;
-                const int jj = tile_of(n), k0 = (kt0 + jj) * TK, info = (tc + jj) & (kInfo - 1);
+                const int jj = tile_of(n), k0 = (p.kt0 + jj) * TK, info = (p.tc + jj) & (kInfo - 1);
                 ok = mbar_wait(&sfull[i], n_s[i] & 1, nullptr, &s_abort);
                 if (!ok) break;
                 ++n_s[i];
                 tc_fence_after();
                 const uint32_t scol = lanes + i * C::S_STEP;
-                uint32_t holes[TK / 32], slow = 0, any = 0;
+                uint32_t slow = 0, any = 0;
 #pragma unroll
                 for (int g = 0; g < TK / 32; ++g) {
                     const uint2 f = *reinterpret_cast<const uint2 *>(flags + info * 8 + g * 2);
-                    holes[g] = f.x;
                     any |= f.x;
                     slow |= f.y;
                 }
                 const bool plain = k0 + TK - 1 <= full_hi && k0 > full_lo && any == 0;
-                auto masked = [&](float (&x)[32], int g) {
-                    const int c0 = k0 + 32 * g;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c0 + e > hi || c0 + e <= lo || (holes[g] >> e & 1)) x[e] = -INFINITY;
-                };
                 const bool has_slow = slow != 0;
-                auto is_slow = [&](int g) { return has_slow && flags[info * 8 + g * 2 + 1] != 0; };
-                auto fetch = [&](float (&x)[32], int g) {
-                    tmem_ld32(scol + 32 * g, x);
-                    tmem_ld_wait();
-                    if (is_slow(g))  // these come out in the unit of M, the others in that of 1 / fac
+                uint64_t sum = pack2(0.f, 0.f);
+                // 32 scores: P from the maximum so far, checked first
+                auto chunk = [&](float (&x)[32], int g) {
+                    const bool own = has_slow && flags[info * 8 + g * 2 + 1] != 0;
+                    if (own) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             x[e] = fmaf(x[e] * kmul[info * TK + 32 * g + e], fac, ve[info * TK + 32 * g + e]);
-                    if (!plain) masked(x, g);
-                };
-                float top = -INFINITY;
+                    }
+                    if (!plain) {
+                        const int c0 = k0 + 32 * g;
+                        const uint32_t hole = flags[info * 8 + g * 2];
 #pragma unroll
-                for (int g = 0; g < TK / 32; ++g) {
-                    float x[32];
-                    fetch(x, g);
-                    float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+                        for (int e = 0; e < 32; ++e)
+                            if (c0 + e > hi || c0 + e <= lo || (hole >> e & 1)) x[e] = -INFINITY;
+                    }
+                    const float fg = own ? 1.f : fac;
+                    float t0 = fmaxf(x[0], x[1]), t1 = fmaxf(x[2], x[3]);
 #pragma unroll
                     for (int e = 4; e < 32; e += 4) {
-                        t0 = fmaxf(t0, x[e]);
-                        t1 = fmaxf(t1, x[e + 1]);
-                        t2 = fmaxf(t2, x[e + 2]);
-                        t3 = fmaxf(t3, x[e + 3]);
+                        t0 = fmaxf(fmaxf(t0, x[e]), x[e + 1]);
+                        t1 = fmaxf(fmaxf(t1, x[e + 2]), x[e + 3]);
                     }
-                    top = fmaxf(top, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * (is_slow(g) ? 1.f : fac));
-                }
-                if (__any_sync(kFullMask, top > M + 11.f)) {
-                    const float m = fmaxf(M, top - 6.f), f = ex2(M - m);
-                    if (SLOTS == 1 && n > 0) {  // the last product may still run: S of this step was issued before it
-                        ok = mbar_wait(&pvdone, (pvc + n - 1) & 1, nullptr, &s_abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    M = m;
-                    l *= f;
-                    if (mine) {
+                    const float top = fmaxf(t0, t1) * fg;
+                    if (__any_sync(kFullMask, top > M + 11.f)) {
+                        // M moves by p.whole numbers: what was computed with the old one is scaled exactly
+                        const float m = fmaxf(M, ceilf(top - 6.f)), f = ex2(M - m);
+                        M = m;
+                        l *= f;
+                        const float2 z = unpack2(sum);
+                        sum = pack2(z.x * f, z.y * f);
+                        const __half2 fh = __float2half2_rn(f);
 #pragma unroll 1
-                        for (int g = 0; g < D / 16; ++g) {
-                            float x[16];
-                            uint32_t y[16];
-                            tmem_ld16(ocol + 16 * g, x);
+                        for (int h = 0; h < g; ++h) {
+                            float y[16];
+                            uint32_t w[16];
+                            tmem_ld16(scol + 16 * h, y);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * f);
-                            tmem_st16(ocol + 16 * g, y);
+                            for (int e = 0; e < 16; ++e) w[e] = h2_bits(__hmul2(bits_h2(__float_as_uint(y[e])), fh));
+                            tmem_st16(scol + 16 * h, w);
+                        }
+                        if (mine) {
+                            if (SLOTS == 1) {  // the last product may still run: S of this step was issued before it
+                                ok = mbar_wait(&pvdone, (p.tc + n - 1) & 1, nullptr, &s_abort) && ok;
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int h = 0; h < D / 16; ++h) {
+                                float y[16];
+                                uint32_t w[16];
+                                tmem_ld16(ocol + 16 * h, y);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e] * f);
+                                tmem_st16(ocol + 16 * h, w);
+                            }
                         }
                     }
-                }
-                const uint64_t m2 = pack2(-M, -M);
-                uint64_t sum = pack2(0.f, 0.f);
-#pragma unroll
-                for (int g = 0; g < TK / 32; ++g) {
-                    float x[32];
-                    fetch(x, g);
-                    const float fg = is_slow(g) ? 1.f : fac;
-                    const uint64_t f2 = pack2(fg, fg);
+                    const uint64_t f2 = pack2(fg, fg), m2 = pack2(-M, -M);
                     uint32_t y[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -583,13 +647,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[e] = ex2(z.x), x[e + 1] = ex2(z.y);
                         y[e / 2] = h2_bits(__floats2half2_rn(x[e], x[e + 1]));
                     }
-                    if (is_slow(g)) {
+                    if (own) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] *= vinv[info * TK + 32 * g + e];
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) sum = add2(sum, pack2(x[e], x[e + 1]));
                     tmem_st16(scol + 16 * g, y);
+                };
+                // P of a chunk lies in columns that were read before; the next chunk comes up meanwhile
+                float xa[32], xb[32];
+                tmem_ld32(scol, xa);
+#pragma unroll 1
+                for (int g = 0; g < TK / 32; g += 2) {
+                    tmem_ld_wait();
+                    tmem_ld32(scol + 32 * g + 32, xb);
+                    chunk(xa, g);
+                    tmem_ld_wait();
+                    if (g + 2 < TK / 32) tmem_ld32(scol + 32 * g + 64, xa);
+                    chunk(xb, g + 1);
                 }
                 const float2 z = unpack2(sum);
                 l += z.x + z.y;
@@ -600,11 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the rows' results
             if (slot < SLOTS) {
-                ok = mbar_wait(&odone, pieces & 1, nullptr, &s_abort) && ok;
+                ok = mbar_wait(&odone, p.count & 1, nullptr, &s_abort) && ok;
                 tc_fence_after();
-                float *other = reinterpret_cast<float *>(sk);  // the second O of a dual item: [D][128 rows]
+                float *other = reinterpret_cast<float *>(sk);  // the second O of a p.dual item: [D][128 rows]
                 float f0 = 1.f, f1 = 0.f;
-                if (dual) {
+                if (p.dual) {
                     if (slot == 1) {
                         sml[tr] = make_float2(M, mine ? l : 0.f);
 #pragma unroll 1
@@ -619,17 +695,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     named_barrier(1, 256);
                     const float2 y = sml[tr];
                     const float m = fmaxf(M, y.x);
-                    f0 = ex2(M - m), f1 = nt > 1 ? ex2(y.x - m) : 0.f;
+                    f0 = ex2(M - m), f1 = p.nt > 1 ? ex2(y.x - m) : 0.f;
                     l = l * f0 + y.y * f1;
                     M = m;
                 }
                 // all lanes of a warp read tensor memory together
-                const bool store = (!dual || slot == 0) && r < it.rows;
+                const bool store = (!p.dual || slot == 0) && r < p.it.rows;
                 // a broken wait must not pass for a result
                 const float bad = ok && !*(volatile int *)&s_abort ? 1.f : NAN;
-                const float norm = whole ? bad * (l > 0.f ? rsqrt_dim<D>() / l : 0.f) : bad;
+                const float norm = p.whole ? bad * (l > 0.f ? rsqrt_dim<D>() / l : 0.f) : bad;
                 f0 *= norm, f1 *= norm;
-                if (!dual || slot == 0) {
+                if (!p.dual || slot == 0) {
                     auto row16 = [&](float (&x)[16], int col) {  // 16 columns, values in order
                         float y[16];
                         tmem_ld16(ocol + col, y);
@@ -637,13 +713,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float z = mine ? y[e] * f0 : 0.f;
-                            if (dual && nt > 1) z = fmaf(other[(col + e) * 128 + tr], f1, z);
+                            if (p.dual && p.nt > 1) z = fmaf(other[(col + e) * 128 + tr], f1, z);
                             x[(e & 8) + value_at(e & 7)] = z;
                         }
                     };
-                    if (whole) {
-                        const int i = (it.row0 + r) / a.group, h = hk * a.group + it.row0 + r - i * a.group;
-                        __nv_bfloat16 *dst = a.out + (s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
+                    if (p.whole) {
+                        const int i = (p.it.row0 + r) / a.group, h = p.hk * a.group + p.it.row0 + r - i * a.group;
+                        __nv_bfloat16 *dst = a.out + (p.s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
                         // H of D = H of D / 64 over H of 64: one 64-value output block at a time
 #pragma unroll 1
                         for (int q = 0; q < D / 64; ++q) {
@@ -677,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     } else {
-                        float *part = parts + (int64_t)((blockIdx.x * 2 + (u ? 1 : 0)) * C::ROWS + r) * C::PART;
+                        float *part = parts + (int64_t)((blockIdx.x * 2 + (p.u ? 1 : 0)) * C::ROWS + r) * C::PART;
 #pragma unroll 1
                         for (int g = 0; g < D / 16; ++g) {
                             float x[16];
@@ -692,39 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            tc_fence_before();
-        }
-
-        // ---- the next piece
-        if (u == first && !whole && threadIdx.x == 0) {
-            // it starts here and ends in the CTA that holds its last unit
-            const int64_t last = u_lo + first + per - 1;
-            int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
-            while (run_start(total, c + 1, ctas) <= last) ++c;
-            spans[blockIdx.x] = Span{c - (int)blockIdx.x + 1, u ? 1 : 0, (int)s.t0, it.rows, hk, it.row0, {0, 0}};
-        }
-        tc += nt;
-        if (SLOTS == 2)
-            sc[0] += dual ? (nt + 1) / 2 : nt, sc[1] += dual ? nt / 2 : nt;
-        else
-            sc[0] += (nt + 1) / 2, sc[1] += nt / 2, pvc += nt;
-        ++pieces;
-        u = u_end;
-        if (u < units) {
-            first += per;
-            if (++rt == item_count(a, s.n, C::ROWS)) {
-                rt = 0;
-                if (++hk == a.c.n_kv_heads) {
-                    hk = 0;
-                    do {
-                        load_seq(s, a, ++b);
-                    } while (s.n == 0);
-                }
-            }
-            it = item_of<D>(a, s, rt);
-        }
-        __syncthreads();
-        if (*(volatile int *)&s_abort) break;
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -740,7 +784,7 @@ cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(k_attn_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     k_attn_tiles<D><<<kSms, kThreads, C::SMEM, st>>>(tab, a);
-    return launch_join<D, C::ROWS>(a, kSms, st);
+    return launch_join<D, C::ROWS, 1>(a, kSms, st);
 }
 
 }  // namespace
