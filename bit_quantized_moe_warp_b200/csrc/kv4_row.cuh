@@ -109,27 +109,66 @@ __device__ __forceinline__ void fwht_warp(float (&v)[D / 32], int lane) {
     }
 }
 
-// One query row for the attention, held by a warp as fwht_warp lays it out:
-// bf16 load, rotary in fp32, H x / sqrt(D), times `scale`.
+// One query row for the attention, held by a warp as fwht_warp lays it out, in
+// three steps: the cosines and sines of a token (which its heads share), the
+// loads, and rotary in fp32 with H x / sqrt(D) * scale.
 template <int D>
-__device__ __forceinline__ void load_query_row(float (&v)[D / 32], const __nv_bfloat16 *x, const RopeTable &t,
-                                              int position, float scale, int lane) {
-    constexpr int P = D / 32;
-    const int i0 = lane * P;
+struct QueryRow {
+    static constexpr int P = D / 32;
+    // value i -> x_i c_i + x_partner s_i
+    static __device__ __forceinline__ void angles(float2 (&cs)[P], const RopeTable &t, int position, int lane) {
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int i = i0 + j;
-        float a = __bfloat162float(x[i]);
-        if (i < t.rd) {
-            const float b = __bfloat162float(x[rope_partner(t, i)]);
-            const float2 cs = rope_cs_f32(t, rope_pair(t, i), position);
-            a = rope_is_second(t, i) ? rope_second(b, a, cs) : rope_first(a, b, cs);
+        for (int j = 0; j < P; ++j) {
+            const int i = lane * P + j;
+            cs[j] = make_float2(1.f, 0.f);
+            if (i < t.rd) {
+                if (!t.half && (j & 1)) {
+                    cs[j] = make_float2(cs[j - 1].x, -cs[j - 1].y);
+                } else {
+                    cs[j] = rope_cs_f32(t, rope_pair(t, i), position);
+                    if (!rope_is_second(t, i)) cs[j].y = -cs[j].y;
+                }
+            }
         }
-        v[j] = a;
     }
-    fwht_warp<D>(v, lane);
+    // the lane's values, and their partners in the half layout
+    struct Raw {
+        uint32_t x[P / 2], y[P / 2];
+    };
+    static __device__ __forceinline__ void words(uint32_t (&w)[P / 2], const __nv_bfloat16 *x) {
+        if constexpr (P == 2) w[0] = *reinterpret_cast<const uint32_t *>(x);
+        if constexpr (P == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(x);
+        if constexpr (P == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(x);
+    }
+    static __device__ __forceinline__ void load(Raw &r, const __nv_bfloat16 *x, const RopeTable &t, int lane) {
+        const int i = lane * P;
+        words(r.x, x + i);
 #pragma unroll
-    for (int j = 0; j < P; ++j) v[j] *= rsqrt_dim<D>() * scale;
-}
+        for (int j = 0; j < P / 2; ++j) r.y[j] = 0u;
+        if (!t.half || i >= t.rd) return;
+        if (t.rd % (2 * P) == 0) {  // the partners of a lane lie together
+            words(r.y, x + rope_partner(t, i));
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                if (i + j < t.rd)
+                    r.y[j / 2] |= (uint32_t)__bfloat16_as_ushort(x[rope_partner(t, i + j)]) << (16 * (j & 1));
+        }
+    }
+    static __device__ __forceinline__ void turn(float (&v)[P], const Raw &r, const float2 (&cs)[P], const RopeTable &t,
+                                                float scale, int lane) {
+        float x[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) x[j] = (j & 1) ? bf16_hi(r.x[j / 2]) : bf16_lo(r.x[j / 2]);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float y = t.half ? ((j & 1) ? bf16_hi(r.y[j / 2]) : bf16_lo(r.y[j / 2])) : x[j ^ 1];
+            v[j] = lane * P + j < t.rd ? fmaf(y, cs[j].y, x[j] * cs[j].x) : x[j];
+        }
+        fwht_warp<D>(v, lane);
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] *= rsqrt_dim<D>() * scale;
+    }
+};
 
 }  // namespace strata

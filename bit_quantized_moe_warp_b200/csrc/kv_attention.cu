@@ -295,8 +295,11 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
             if (r < rows) {
                 const int i = (row0 + r) / a.group, h = hk * a.group + (row0 + r) - i * a.group;
                 const int64_t tok = s.t0 + i;
-                load_query_row<D>(v, a.q + tok * a.d.q_token_stride + (int64_t)h * D, tab,
-                                  tab.rd ? a.positions[tok] : 0, 1.f, lane);
+                typename QueryRow<D>::Raw raw;
+                float2 cs[P];
+                QueryRow<D>::load(raw, a.q + tok * a.d.q_token_stride + (int64_t)h * D, tab, lane);
+                QueryRow<D>::angles(cs, tab, tab.rd ? a.positions[tok] : 0, lane);
+                QueryRow<D>::turn(v, raw, cs, tab, 1.f, lane);
             }
             float m = 0.f;
 #pragma unroll

@@ -26,8 +26,6 @@
 //
 // Work: the key tiles of all items in a row, cut into 148 equal runs, one for
 // each CTA; pieces of an item that several CTAs share go through k_attn_join.
-#include <type_traits>
-
 #include "kv_attn.cuh"
 
 namespace strata {
@@ -89,6 +87,20 @@ STRATA_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         : "memory");
 }
 STRATA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// by a whole warp, which goes on or gives up together
+STRATA_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(kFullMask, mbar_wait(bar, parity, nullptr, abort));
+}
+// barrier of `threads` threads; whether any of them says stop
+STRATA_DEV bool named_barrier_or(int id, int threads, bool stop) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"((uint32_t)stop)
+        : "memory");
+    return any != 0;
+}
 STRATA_DEV void named_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // Operand with the other dimension contiguous (V: 64 values of a key, 128-byte
@@ -165,7 +177,7 @@ struct Piece {
     SeqBase s;
     Item it;
     int kt0, nt, steps;
-    bool whole, dual;
+    bool whole, dual, after_dual;
     uint32_t tc, sc[2], count;  // key tiles, steps in each S, pieces so far: buffers and phases
 };
 
@@ -194,13 +206,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           *vinv = reinterpret_cast<float *>(aux + C::VINV), *sfac = reinterpret_cast<float *>(aux + C::FAC);
     uint32_t *flags = reinterpret_cast<uint32_t *>(aux + C::FLAGS);  // [kInfo][4 groups of 32 keys](holes, slow)
     float2 *sml = reinterpret_cast<float2 *>(aux + C::ML);
-    __shared__ uint64_t kfull[2], vfull[2], kempty[2], vempty[2], sfull[2], pready[2], pvdone, odone;
+    __shared__ uint64_t kfull[2], vfull[2], kempty[2], vempty[2], sfull[2], pready[2], pvdone, odone, qfull;
     __shared__ uint32_t tmem_base;
     __shared__ int s_abort, s_b;
     __shared__ int64_t s_sum[kThreads / 32], s_before;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     griddep_launch_dependents();
 
+    // rows that no item fills stay finite
+    for (int i = threadIdx.x; i < SLOTS * C::Q / 16; i += kThreads) reinterpret_cast<uint4 *>(sq)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < C::ROWS; i += kThreads) sfac[i] = 1.f;
+    fence_proxy_async_smem();
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&kfull[i], 4);
@@ -212,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&pvdone, 1);
         mbar_init(&odone, 1);
+        mbar_init(&qfull, 8);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -307,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)0x80000000);
 
     // Every role walks over the pieces by itself, with its own registers.
-    // load_q: the warps that bring the query rows.
-    auto pieces = [&](auto load_q, auto &&role) {
+    auto pieces = [&](auto &&role) {
     Piece p{};
     p.b = b, p.hk = hk, p.rt = rt, p.first = first, p.s = s, p.it = it;
     for (; p.u < units;) {
@@ -320,42 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.dual = SLOTS == 2 && p.it.rows <= 128;
         p.steps = SLOTS == 2 && !p.dual ? 2 * p.nt : p.nt;
 
-        if constexpr (decltype(load_q)::value) {
-        // ---- query rows: rotary, transform, fp16 with a power-of-two scale
-        const int q_rows = p.dual || SLOTS == 1 ? 128 : 256;
-        for (int r = warp; r < q_rows; r += kMmaWarp) {
-            float q[P];
-#pragma unroll
-            for (int i = 0; i < P; ++i) q[i] = 0.f;
-            if (r < p.it.rows) {
-                const int i = (p.it.row0 + r) / a.group, h = p.hk * a.group + (p.it.row0 + r) - i * a.group;
-                const int64_t tok = p.s.t0 + i;
-                load_query_row<D>(q, a.q + tok * a.d.q_token_stride + (int64_t)h * D, tab,
-                                  tab.rd ? a.positions[tok] : 0, a.scale_log2 < 0.f ? -1.f : 1.f, lane);
-            }
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(q[i]));
-#pragma unroll
-            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-            const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 252u);
-            const float mul = m > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int d = lane * P + i;
-                *reinterpret_cast<__half *>(sq + (r >> 7) * C::Q + sw_chunk(128, r & 127, d >> 3) + place_of(d & 7) * 2) =
-                    __float2half_rn(q[i] * mul);
-            }
-            // above zero, so that a masked score stays -inf
-            if (lane == 0) sfac[r] = fmaxf(fabsf(a.scale_log2) * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
-        }
-        fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        named_barrier(0, kThreads);
-        tc_fence_after();
-
-        role(p);
+        if (!role(p)) break;
         // ---- the next piece
         if (p.u == p.first && !p.whole && threadIdx.x == 0) {
             // it starts here and ends in the CTA that holds its last unit
@@ -370,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
             p.sc[0] += (p.nt + 1) / 2, p.sc[1] += p.nt / 2;
         ++p.count;
+        if (p.nt > 0) p.after_dual = p.dual;
         p.u = p.u_end;
         if (p.u < units) {
             p.first += per;
@@ -384,62 +366,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             p.it = item_of<D>(a, p.s, p.rt);
         }
-        tc_fence_before();
-        named_barrier(0, kThreads);
-        tc_fence_after();
-        if (*(volatile int *)&s_abort) break;
     }
     };
 
     if (warp >= kMmaWarp) {
         regs_down<64>();
-        pieces(std::false_type{}, [&](const Piece &p) {
+        if (warp == kMmaWarp && lane == 0) pieces([&](const Piece &p) {
         auto tile_of = [&](int n) { return SLOTS == 2 && !p.dual ? n >> 1 : n; };  // of step n, in S n & 1
             // ------------------------------------------------ matrix products
-            if (warp == kMmaWarp && lane == 0) {
-                constexpr uint32_t idesc_s = umma_idesc_f16(128, TK), idesc_o = umma_idesc_f16(128, D) | (1u << 16);
-                bool ok = true;
-                uint32_t s_n[2] = {p.sc[0], p.sc[1]};
-                auto product_s = [&](int n) {
-                    const uint32_t c = p.tc + tile_of(n), i = n & 1;
-                    if (!mbar_wait(&kfull[c & 1], (c >> 1) & 1, nullptr, &s_abort)) return false;
-                    tc_fence_after();
-                    const uint64_t qd = umma_desc_sw128(sq + (SLOTS == 2 && !p.dual ? i : 0) * C::Q);
-                    const uint64_t kd = umma_desc_sw128(sk + (c & 1) * C::KV);
+            constexpr uint32_t idesc_s = umma_idesc_f16(128, TK), idesc_o = umma_idesc_f16(128, D) | (1u << 16);
+            // the rows are there, and what the last piece left in tensor memory has been read
+            bool ok = mbar_wait(&qfull, p.count & 1, nullptr, &s_abort);
+            tc_fence_after();
+            uint32_t s_n[2] = {p.sc[0], p.sc[1]};
+            auto product_s = [&](int n) {
+                const uint32_t c = p.tc + tile_of(n), i = n & 1;
+                if (!mbar_wait(&kfull[c & 1], (c >> 1) & 1, nullptr, &s_abort)) return false;
+                tc_fence_after();
+                const uint64_t qd = umma_desc_sw128(sq + (SLOTS == 2 && !p.dual ? i : 0) * C::Q);
+                const uint64_t kd = umma_desc_sw128(sk + (c & 1) * C::KV);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        umma_f16(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
-                                 kd + (k >> 2) * (TK * 128 / 16) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
-                    umma_commit(&sfull[i]);
-                    if (SLOTS == 1 || p.dual || i) umma_commit(&kempty[c & 1]);
-                    return true;
-                };
-                for (int n = 0; n < 2 && n < p.steps && ok; ++n) ok = product_s(n);
-                for (int n = 0; n < p.steps && ok; ++n) {
-                    const uint32_t c = p.tc + tile_of(n), i = n & 1;
-                    ok = mbar_wait(&vfull[c & 1], (c >> 1) & 1, nullptr, &s_abort) &&
-                         mbar_wait(&pready[i], s_n[i] & 1, nullptr, &s_abort);
-                    if (!ok) break;
-                    ++s_n[i];
-                    tc_fence_after();
-                    const uint64_t vd = umma_desc_sw128_mn(sv + (c & 1) * C::KV, TK * 128);
-                    const bool fresh = SLOTS == 2 ? n < 2 : n == 0;
+                for (int k = 0; k < D / 16; ++k)
+                    umma_f16(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
+                             kd + (k >> 2) * (TK * 128 / 16) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
+                umma_commit(&sfull[i]);
+                if (SLOTS == 1 || p.dual || i) umma_commit(&kempty[c & 1]);
+                return true;
+            };
+            for (int n = 0; n < 2 && n < p.steps && ok; ++n) ok = product_s(n);
+            for (int n = 0; n < p.steps && ok; ++n) {
+                const uint32_t c = p.tc + tile_of(n), i = n & 1;
+                ok = mbar_wait(&vfull[c & 1], (c >> 1) & 1, nullptr, &s_abort) &&
+                     mbar_wait(&pready[i], s_n[i] & 1, nullptr, &s_abort);
+                if (!ok) break;
+                ++s_n[i];
+                tc_fence_after();
+                const uint64_t vd = umma_desc_sw128_mn(sv + (c & 1) * C::KV, TK * 128);
+                const bool fresh = SLOTS == 2 ? n < 2 : n == 0;
 #pragma unroll
-                    for (int k = 0; k < TK / 16; ++k)
-                        umma_ts(tbase + C::O_COL + (SLOTS == 2 ? i * D : 0), tbase + i * C::S_STEP + k * 8,
-                                vd + k * (2048 / 16), idesc_o, fresh && k == 0 ? 0u : 1u);
-                    if (SLOTS == 1) umma_commit(&pvdone);
-                    if (SLOTS == 1 || p.dual || i) umma_commit(&vempty[c & 1]);
-                    if (n + 2 < p.steps) ok = product_s(n + 2);
-                }
-                umma_commit(&odone);
-                mbar_wait(&odone, p.count & 1, nullptr, nullptr);  // before anything is torn down
+                for (int k = 0; k < TK / 16; ++k)
+                    umma_ts(tbase + C::O_COL + (SLOTS == 2 ? i * D : 0), tbase + i * C::S_STEP + k * 8,
+                            vd + k * (2048 / 16), idesc_o, fresh && k == 0 ? 0u : 1u);
+                if (SLOTS == 1) umma_commit(&pvdone);
+                if (SLOTS == 1 || p.dual || i) umma_commit(&vempty[c & 1]);
+                if (n + 2 < p.steps) ok = product_s(n + 2);
             }
-            __syncwarp();
+            umma_commit(&odone);
+            mbar_wait(&odone, p.count & 1, nullptr, nullptr);  // before anything is torn down
+            return ok;
         });
     } else if (warp >= 8) {
         regs_down<80>();
-        pieces(std::true_type{}, [&](const Piece &p) {
+        pieces([&](const Piece &p) {
             // ------------------------------------------------ expanding keys (warps 8-11) and values (12-15)
             const bool is_v = warp >= 12;
             const int id = threadIdx.x - (is_v ? 384 : 256), row = id % TK, part = id / TK;
@@ -475,6 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             find(0);
             load(0);
             find(1);
+            // the second O of the last piece was added up in the keys' buffers
+            if (p.nt > 0 && p.after_dual && !warp_wait(&qfull, p.count & 1, &s_abort)) return false;
             for (int jj = 0; jj < p.nt; ++jj) {
                 const uint32_t c = p.tc + jj;
                 // the scales' ranges decide for 32 keys at a time; keys and values see the same numbers
@@ -516,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load(jj + 1);
                 find(jj + 2);
                 uint64_t *full = is_v ? &vfull[c & 1] : &kfull[c & 1], *empty = is_v ? &vempty[c & 1] : &kempty[c & 1];
-                if (!mbar_wait(empty, ((c >> 1) & 1) ^ 1, nullptr, &s_abort)) break;
+                if (!warp_wait(empty, ((c >> 1) & 1) ^ 1, &s_abort)) return false;
                 uint8_t *to = (is_v ? sv : sk) + (c & 1) * C::KV;
                 if (slow) {
                     const __half2 mul = bits_h2((uint32_t)(15 - e) * 0x04000400u);  // 2^-e, -15 <= e <= 14
@@ -543,12 +523,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);
             }
+            return true;
         });
     } else {
         regs_up<128>();
-        pieces(std::true_type{}, [&](const Piece &p) {
+        pieces([&](const Piece &p) {
         auto tile_of = [&](int n) { return SLOTS == 2 && !p.dual ? n >> 1 : n; };  // of step n, in S n & 1
             // ------------------------------------------------ softmax: S slot (warps 0-3, 4-7), a thread per row
+            // the rows first: rotary, transform, fp16 with a power-of-two scale; a warp
+            // takes rows in a run, which share a token's angles
+            {
+                using Q = QueryRow<D>;
+                constexpr int BATCH = D == 256 ? 2 : 4;
+                const int q_rows = p.dual || SLOTS == 1 ? 128 : 256, run = q_rows / 8;
+                float2 cs[P];
+                int64_t at = -1;
+                for (int r0 = warp * run; r0 < warp * run + run; r0 += BATCH) {
+                    typename Q::Raw raw[BATCH];
+                    int64_t tok[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int row = p.it.row0 + min(r0 + k, p.it.rows - 1);
+                        const int i = row / a.group;
+                        tok[k] = p.s.t0 + i;
+                        Q::load(raw[k], a.q + tok[k] * a.d.q_token_stride + (int64_t)(p.hk * a.group + row - i * a.group) * D,
+                                tab, lane);
+                    }
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int r = r0 + k;
+                        if (tok[k] != at) {
+                            at = tok[k];
+                            Q::angles(cs, tab, tab.rd ? a.positions[at] : 0, lane);
+                        }
+                        float q[P], m = 0.f;
+                        Q::turn(q, raw[k], cs, tab, a.scale_log2 < 0.f ? -1.f : 1.f, lane);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(q[i]));
+#pragma unroll
+                        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
+                        const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 252u);
+                        const float mul = m > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            const int d = lane * P + i;
+                            *reinterpret_cast<__half *>(sq + (r >> 7) * C::Q + sw_chunk(128, r & 127, d >> 3) +
+                                                        place_of(d & 7) * 2) = __float2half_rn(q[i] * mul);
+                        }
+                        // above zero, so that a masked score stays -inf
+                        if (lane == 0)
+                            sfac[r] = fmaxf(fabsf(a.scale_log2) * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
+                    }
+                    if (r0 + BATCH >= p.it.rows) break;  // what lies behind keeps older rows' values: finite, never stored
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                // the factors are read by other warps; a wait that ran out ends the work for all of them
+                if (named_barrier_or(2, 256, *(volatile int *)&s_abort != 0)) return false;
+                if (lane == 0) mbar_arrive(&qfull);
+            }
             const int slot = warp >> 2, tr = threadIdx.x & 127;
             const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
             const uint32_t ocol = lanes + C::O_COL + (SLOTS == 2 ? slot * D : 0);
@@ -566,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = slot; n < p.steps && slot < SLOTS; n += SLOTS, ++mine) {
                 const int i = SLOTS == 2 ? slot : n & 1;
                 const int jj = tile_of(n), k0 = (p.kt0 + jj) * TK, info = (p.tc + jj) & (kInfo - 1);
-                ok = mbar_wait(&sfull[i], n_s[i] & 1, nullptr, &s_abort);
+                ok = warp_wait(&sfull[i], n_s[i] & 1, &s_abort);
                 if (!ok) break;
                 ++n_s[i];
                 tc_fence_after();
@@ -624,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (mine) {
                             if (SLOTS == 1) {  // the last product may still run: S of this step was issued before it
-                                ok = mbar_wait(&pvdone, (p.tc + n - 1) & 1, nullptr, &s_abort) && ok;
+                                ok = warp_wait(&pvdone, (p.tc + n - 1) & 1, &s_abort) && ok;
                                 tc_fence_after();
                             }
 #pragma unroll 1
@@ -675,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&pready[i]);
             }
             // ---- the rows' results
+            ok = warp_wait(&odone, p.count & 1, &s_abort) && ok;  // the next piece's rows overwrite these, too
             if (slot < SLOTS) {
-                ok = mbar_wait(&odone, p.count & 1, nullptr, &s_abort) && ok;
                 tc_fence_after();
                 float *other = reinterpret_cast<float *>(sk);  // the second O of a p.dual item: [D][128 rows]
                 float f0 = 1.f, f1 = 0.f;
@@ -768,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            return true;
         });
     }
     tc_fence_before();
