@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
     settle();
     // from here on units count from u_lo
     int per = seq_units(s);
-    int vh = uniform((int)((u_lo - s_before) / per));  // (KV head, row group) inside the sequence
+    int vh = uniform((int)run_start(u_lo - s_before, 1, per));  // (KV head, row group) inside the sequence
     int first = uniform((int)(s_before + (int64_t)vh * per - u_lo));  // its first unit
     const int units = uniform((int)(u_hi - u_lo));
     const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)0x80000000);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
 #pragma unroll
             for (int i = 0; i < P; ++i) v[i] = 0.f;
             if (r < rows) {
-                const int i = (row0 + r) / a.group, h = hk * a.group + (row0 + r) - i * a.group;
+                const int i = by_group(a, row0 + r), h = hk * a.group + (row0 + r) - i * a.group;
                 const int64_t tok = s.t0 + i;
                 typename QueryRow<D>::Raw raw;
                 float2 cs[P];
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
             for (int j = 0; j < 2; ++j) {
                 const int r = n * 8 + 2 * t + j;
                 fac[n][j] = sfac[r];
-                const int p = p_first + (row0 + r) / a.group;
+                const int p = p_first + by_group(a, row0 + r);
                 hi[n][j] = min(p, s.L - 1);
                 lo[n][j] = a.d.window > 0 ? (int)max((int64_t)p - a.d.window, (int64_t)-1) : -1;
                 M[n][j] = -FLT_MAX;
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                 for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
         }
         // tiles up to here, and from there on, need no mask
-        const int last_row = (row0 + rows - 1) / a.group;
-        const int full_hi = p_first + row0 / a.group;
+        const int last_row = by_group(a, row0 + rows - 1);
+        const int full_hi = p_first + by_group(a, row0);
         const int full_lo = a.d.window > 0 ? (int)max((int64_t)p_first + last_row - a.d.window, (int64_t)-1) : -1;
 
         // word t of block 0 of key g; word g / 2 of block 0 of key 2t, and the half of it with values 4g .. 4g + 3
@@ -691,8 +691,9 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
     static const RopeTable none = {};
     const RopeTable &tab = rope ? rope->table : none;
     AttnArgs a{*cache, *d, positions, static_cast<const __nv_bfloat16 *>(q), q_offsets, kv_lens, block_table,
-               static_cast<__nv_bfloat16 *>(out), workspace, d->n_q_heads / cache->n_kv_heads, 0, 0.f};
+               static_cast<__nv_bfloat16 *>(out), workspace, d->n_q_heads / cache->n_kv_heads, 0, 0.f, 0};
     while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
+    a.group_inv = a.group > 1 ? ~0ull / (uint64_t)a.group + 1 : 0;
     a.scale_log2 = d->scale * 1.44269504088896340736f;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool two = (int64_t)d->max_q_len * a.group > 8;

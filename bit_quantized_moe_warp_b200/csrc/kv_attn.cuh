@@ -21,7 +21,14 @@ struct AttnArgs {
     void *workspace;
     int group, page_shift;
     float scale_log2;  // scale * log2(e)
+    uint64_t group_inv;  // 2^64 / group, rounded up (0 for 1)
 };
+// row / group for 0 <= row < 2^31: exact, since the rounding of group_inv adds
+// less than 2^31 / 2^64 of the divisor's reciprocal
+__device__ __forceinline__ int by_group(const AttnArgs &a, int row) {
+    return a.group_inv ? (int)__umul64hi((uint64_t)(uint32_t)row, a.group_inv) : row;
+}
+
 // Row r of a KV head's query rows (token-major, the group's heads inside), in
 // the rotated basis: back through the transform, divided by its sum, rounded
 // once.
@@ -29,7 +36,7 @@ template <int D>
 __device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[D / 32], float l, int64_t t0, int hk, int r,
                                           int lane) {
     constexpr int P = D / 32;
-    const int i = r / a.group, h = hk * a.group + r - i * a.group;
+    const int i = by_group(a, r), h = hk * a.group + r - i * a.group;
     const float f = l > 0.f ? rsqrt_dim<D>() / l : 0.f;
     fwht_warp<D>(v, lane);
     uint32_t w[P / 2];
@@ -52,7 +59,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // total * i / n, rounded down: where run i of n starts
 __device__ __forceinline__ int64_t run_start(int64_t total, int64_t i, int64_t n) {
-    return (int64_t)((uint64_t)total * (uint64_t)i / (uint64_t)n);
+    const uint64_t x = (uint64_t)total * (uint64_t)i;
+    return ((x | (uint64_t)n) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)n) : (int64_t)(x / (uint64_t)n);
 }
 
 // A sequence: its first query row, query rows and cached tokens, in range

@@ -161,7 +161,7 @@ STRATA_DEV Item item_of(const AttnArgs &a, const SeqBase &s, int rt) {
     Item it;
     it.row0 = rt * C::ROWS;
     it.rows = min(C::ROWS, s.n * a.group - it.row0);
-    const int first = it.row0 / a.group, last = (it.row0 + it.rows - 1) / a.group;
+    const int first = by_group(a, it.row0), last = by_group(a, it.row0 + it.rows - 1);
     const int hi = max(s.L - s.n + last + 1, 0);
     const int lo = a.d.window > 0 ? (int)max((int64_t)0, (int64_t)s.L - s.n + first - a.d.window + 1) : 0;
     it.tile0 = min(lo, hi) / C::TK;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     {
         const int64_t per = head_units<D>(a, s, lane);
-        hk = uniform((int)((u_lo - s_before) / per));
+        hk = uniform((int)run_start(u_lo - s_before, 1, per));
         int64_t rem = u_lo - s_before - hk * per;
         for (;; rt += 32) {  // the item that holds unit `rem`
             const int n = rt + lane < item_count(a, s.n, C::ROWS) ? item_units(item_of<D>(a, s, rt + lane)) : 0;
@@ -534,27 +534,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             // takes rows in a run, which share a token's angles
             {
                 using Q = QueryRow<D>;
-                constexpr int BATCH = D == 256 ? 2 : 4;
-                const int q_rows = p.dual || SLOTS == 1 ? 128 : 256, run = q_rows / 8;
+                constexpr int BATCH = D == 256 ? 4 : 8;
+                const int run = (min(p.it.rows, p.dual || SLOTS == 1 ? 128 : 256) + 7) / 8;  // 32 at most
+                const int end = min(warp * run + run, p.it.rows);
+                auto tok_of = [&](int r) { return p.s.t0 + by_group(a, p.it.row0 + min(r, p.it.rows - 1)); };
+                const int pos_lane = tab.rd ? a.positions[tok_of(warp * run + lane)] : 0;
                 float2 cs[P];
                 int64_t at = -1;
-                for (int r0 = warp * run; r0 < warp * run + run; r0 += BATCH) {
+                for (int r0 = warp * run; r0 < end; r0 += BATCH) {
                     typename Q::Raw raw[BATCH];
-                    int64_t tok[BATCH];
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {
-                        const int row = p.it.row0 + min(r0 + k, p.it.rows - 1);
-                        const int i = row / a.group;
-                        tok[k] = p.s.t0 + i;
-                        Q::load(raw[k], a.q + tok[k] * a.d.q_token_stride + (int64_t)(p.hk * a.group + row - i * a.group) * D,
+                        const int row = p.it.row0 + min(r0 + k, p.it.rows - 1), i = by_group(a, row);
+                        Q::load(raw[k], a.q + (p.s.t0 + i) * a.d.q_token_stride + (int64_t)(p.hk * a.group + row - i * a.group) * D,
                                 tab, lane);
                     }
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {
                         const int r = r0 + k;
-                        if (tok[k] != at) {
-                            at = tok[k];
-                            Q::angles(cs, tab, tab.rd ? a.positions[at] : 0, lane);
+                        if (r >= end) break;  // what lies behind keeps older rows' values: finite, never stored
+                        if (tok_of(r) != at) {
+                            at = tok_of(r);
+                            Q::angles(cs, tab, __shfl_sync(kFullMask, pos_lane, r - warp * run), lane);
                         }
                         float q[P], m = 0.f;
                         Q::turn(q, raw[k], cs, tab, a.scale_log2 < 0.f ? -1.f : 1.f, lane);
@@ -574,7 +575,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0)
                             sfac[r] = fmaxf(fabsf(a.scale_log2) * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
                     }
-                    if (r0 + BATCH >= p.it.rows) break;  // what lies behind keeps older rows' values: finite, never stored
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -586,11 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
             const uint32_t ocol = lanes + C::O_COL + (SLOTS == 2 ? slot * D : 0);
             const int r = (SLOTS == 2 && !p.dual ? slot * 128 : 0) + tr;  // of the item
-            const int pos = p.s.L - p.s.n + (p.it.row0 + min(r, p.it.rows - 1)) / a.group;
+            const int pos = p.s.L - p.s.n + by_group(a, p.it.row0 + min(r, p.it.rows - 1));
             const int hi = min(pos, p.s.L - 1), lo = a.d.window > 0 ? (int)max((int64_t)pos - a.d.window, (int64_t)-1) : -1;
-            const int full_hi = p.s.L - p.s.n + p.it.row0 / a.group;
+            const int full_hi = p.s.L - p.s.n + by_group(a, p.it.row0);
             const int full_lo =
-                a.d.window > 0 ? (int)max((int64_t)p.s.L - p.s.n + (p.it.row0 + p.it.rows - 1) / a.group - a.d.window, (int64_t)-1) : -1;
+                a.d.window > 0 ? (int)max((int64_t)p.s.L - p.s.n + by_group(a, p.it.row0 + p.it.rows - 1) - a.d.window, (int64_t)-1) : -1;
             const float fac = sfac[r];
             float M = -FLT_MAX, l = 0.f;
             uint32_t n_s[2] = {p.sc[0], p.sc[1]};
@@ -612,66 +612,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slow |= f.y;
                 }
                 const bool plain = k0 + TK - 1 <= full_hi && k0 > full_lo && any == 0;
-                const bool has_slow = slow != 0;
-                uint64_t sum = pack2(0.f, 0.f);
-                // 32 scores: P from the maximum so far, checked first
-                auto chunk = [&](float (&x)[32], int g) {
-                    const bool own = has_slow && flags[info * 8 + g * 2 + 1] != 0;
-                    if (own) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            x[e] = fmaf(x[e] * kmul[info * TK + 32 * g + e], fac, ve[info * TK + 32 * g + e]);
-                    }
-                    if (!plain) {
-                        const int c0 = k0 + 32 * g;
-                        const uint32_t hole = flags[info * 8 + g * 2];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c0 + e > hi || c0 + e <= lo || (hole >> e & 1)) x[e] = -INFINITY;
-                    }
-                    const float fg = own ? 1.f : fac;
-                    float t0 = fmaxf(x[0], x[1]), t1 = fmaxf(x[2], x[3]);
-#pragma unroll
-                    for (int e = 4; e < 32; e += 4) {
-                        t0 = fmaxf(fmaxf(t0, x[e]), x[e + 1]);
-                        t1 = fmaxf(fmaxf(t1, x[e + 2]), x[e + 3]);
-                    }
-                    const float top = fmaxf(t0, t1) * fg;
-                    if (__any_sync(kFullMask, top > M + 11.f)) {
-                        // M moves by p.whole numbers: what was computed with the old one is scaled exactly
-                        const float m = fmaxf(M, ceilf(top - 6.f)), f = ex2(M - m);
-                        M = m;
-                        l *= f;
-                        const float2 z = unpack2(sum);
-                        sum = pack2(z.x * f, z.y * f);
-                        const __half2 fh = __float2half2_rn(f);
+                uint64_t sum[2] = {0, 0};
+                // M moves by whole numbers: what was computed with the old one (chunks before g, O) is scaled exactly
+                auto move = [&](float top, int g) {
+                    const float m = fmaxf(M, ceilf(top - 6.f)), f = ex2(M - m);
+                    M = m;
+                    l *= f;
+                    const uint64_t ff = pack2(f, f);
+                    sum[0] = fma2(sum[0], ff, 0), sum[1] = fma2(sum[1], ff, 0);
+                    const __half2 fh = __float2half2_rn(f);
 #pragma unroll 1
-                        for (int h = 0; h < g; ++h) {
-                            float y[16];
-                            uint32_t w[16];
-                            tmem_ld16(scol + 16 * h, y);
-                            tmem_ld_wait();
+                    for (int h = 0; h < g; ++h) {
+                        float y[16];
+                        uint32_t w[16];
+                        tmem_ld16(scol + 16 * h, y);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = h2_bits(__hmul2(bits_h2(__float_as_uint(y[e])), fh));
-                            tmem_st16(scol + 16 * h, w);
-                        }
-                        if (mine) {
-                            if (SLOTS == 1) {  // the last product may still run: S of this step was issued before it
-                                ok = warp_wait(&pvdone, (p.tc + n - 1) & 1, &s_abort) && ok;
-                                tc_fence_after();
-                            }
-#pragma unroll 1
-                            for (int h = 0; h < D / 16; ++h) {
-                                float y[16];
-                                uint32_t w[16];
-                                tmem_ld16(ocol + 16 * h, y);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e] * f);
-                                tmem_st16(ocol + 16 * h, w);
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e) w[e] = h2_bits(__hmul2(bits_h2(__float_as_uint(y[e])), fh));
+                        tmem_st16(scol + 16 * h, w);
                     }
+                    if (!mine) return;
+                    if (SLOTS == 1) {  // the last product may still run: S of this step was issued before it
+                        ok = warp_wait(&pvdone, (p.tc + n - 1) & 1, &s_abort) && ok;
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int h = 0; h < D / 16; ++h) {
+                        float y[16];
+                        uint32_t w[16];
+                        tmem_ld16(ocol + 16 * h, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e] * f);
+                        tmem_st16(ocol + 16 * h, w);
+                    }
+                };
+                auto largest = [&](const float (&x)[32]) {
+                    float t[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        t[k] = fmaxf(x[8 * k], x[8 * k + 1]);
+#pragma unroll
+                        for (int e = 2; e < 8; e += 2) t[k] = fmaxf(fmaxf(t[k], x[8 * k + e]), x[8 * k + e + 1]);
+                    }
+                    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                };
+                // weights of 32 scores, P into columns that were read before
+                auto weigh = [&](float (&x)[32], int g, float fg) {
                     const uint64_t f2 = pack2(fg, fg), m2 = pack2(-M, -M);
                     uint32_t y[16];
 #pragma unroll
@@ -680,27 +667,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[e] = ex2(z.x), x[e + 1] = ex2(z.y);
                         y[e / 2] = h2_bits(__floats2half2_rn(x[e], x[e + 1]));
                     }
-                    if (own) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] *= vinv[info * TK + 32 * g + e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) sum = add2(sum, pack2(x[e], x[e + 1]));
                     tmem_st16(scol + 16 * g, y);
                 };
-                // P of a chunk lies in columns that were read before; the next chunk comes up meanwhile
-                float xa[32], xb[32];
-                tmem_ld32(scol, xa);
+                auto add = [&](const float (&x)[32]) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) sum[e / 2 & 1] = add2(sum[e / 2 & 1], pack2(x[e], x[e + 1]));
+                };
+                if (plain && slow == 0) {
+                    auto chunk = [&](float (&x)[32], int g) {
+                        const float top = largest(x) * fac;
+                        if (__any_sync(kFullMask, top > M + 11.f)) move(top, g);
+                        weigh(x, g, fac);
+                        add(x);
+                    };
+                    // the next chunk comes up meanwhile
+                    float xa[32], xb[32];
+                    tmem_ld32(scol, xa);
+#pragma unroll
+                    for (int g = 0; g < TK / 32; g += 2) {
+                        tmem_ld_wait();
+                        tmem_ld32(scol + 32 * g + 32, xb);
+                        chunk(xa, g);
+                        tmem_ld_wait();
+                        if (g + 2 < TK / 32) tmem_ld32(scol + 32 * g + 64, xa);
+                        chunk(xb, g + 1);
+                    }
+                } else {
 #pragma unroll 1
-                for (int g = 0; g < TK / 32; g += 2) {
-                    tmem_ld_wait();
-                    tmem_ld32(scol + 32 * g + 32, xb);
-                    chunk(xa, g);
-                    tmem_ld_wait();
-                    if (g + 2 < TK / 32) tmem_ld32(scol + 32 * g + 64, xa);
-                    chunk(xb, g + 1);
+                    for (int g = 0; g < TK / 32; ++g) {
+                        float x[32];
+                        tmem_ld32(scol + 32 * g, x);
+                        tmem_ld_wait();
+                        const bool own = flags[info * 8 + g * 2 + 1] != 0;
+                        const float fg = own ? 1.f : fac;
+                        if (own) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = fmaf(x[e] * kmul[info * TK + 32 * g + e], fac, ve[info * TK + 32 * g + e]);
+                        }
+                        const int c0 = k0 + 32 * g;
+                        const uint32_t hole = flags[info * 8 + g * 2];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c0 + e > hi || c0 + e <= lo || (hole >> e & 1)) x[e] = -INFINITY;
+                        const float top = largest(x) * fg;
+                        if (__any_sync(kFullMask, top > M + 11.f)) move(top, g);
+                        weigh(x, g, fg);
+                        if (own) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] *= vinv[info * TK + 32 * g + e];
+                        }
+                        add(x);
+                    }
                 }
-                const float2 z = unpack2(sum);
+                const float2 z = unpack2(add2(sum[0], sum[1]));
                 l += z.x + z.y;
                 tmem_st_wait();
                 tc_fence_before();
@@ -751,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     if (p.whole) {
-                        const int i = (p.it.row0 + r) / a.group, h = p.hk * a.group + p.it.row0 + r - i * a.group;
+                        const int i = by_group(a, p.it.row0 + r), h = p.hk * a.group + p.it.row0 + r - i * a.group;
                         __nv_bfloat16 *dst = a.out + (p.s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
                         // H of D = H of D / 64 over H of 64: one 64-value output block at a time
 #pragma unroll 1
