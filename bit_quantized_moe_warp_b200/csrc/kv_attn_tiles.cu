@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 20 * 32;  // the last three warps only complete a group of four
 constexpr int kMmaWarp = 16;
+constexpr int kPoly = 3;  // of 8 exponentials, by polynomial
 constexpr int kInfo = 4;  // tiles whose flags are kept
 
 template <int D>
@@ -55,12 +56,36 @@ struct Tiles {
     static_assert(128 * D * 4 <= 4 * KV, "the second O fits the tiles' buffers");
 };
 
-STRATA_DEV void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// The matrix warp runs as one, so that descriptors stay in uniform registers;
+// the instructions themselves are issued by its elected thread.
+STRATA_DEV uint32_t elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+STRATA_DEV void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate, uint32_t me) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(me)
+        : "memory");
+}
+STRATA_DEV void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate, uint32_t me) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(me)
+        : "memory");
+}
+STRATA_DEV void umma_done(uint64_t *bar, uint32_t me) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(me)
         : "memory");
 }
 // 32 lanes x 32 bits, 32 consecutive columns per thread
@@ -136,6 +161,23 @@ STRATA_DEV uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// 2^z of two numbers up to 127 on the fused multiply-add units, for a share of
+// the exponentials: z = n + f with n the nearest integer, 2^f by a polynomial
+// of degree 4 (Remez' minimax in the relative error, 2^-18.5), n into the
+// exponent. Below 2^-126 the result is a number near 2^-126.
+STRATA_DEV float2 ex2_pair(uint64_t z2) {
+    float2 z = unpack2(z2);
+    z2 = pack2(fmaxf(z.x, -126.f), fmaxf(z.y, -126.f));
+    const uint64_t t = add2(z2, pack2(12582912.f, 12582912.f));  // 1.5 * 2^23: the sum's last bits are n
+    const uint64_t f = fma2(add2(t, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), z2);
+    uint64_t r = fma2(f, pack2(0x1.3997d6p-7f, 0x1.3997d6p-7f), pack2(0x1.ca1444p-5f, 0x1.ca1444p-5f));
+    r = fma2(r, f, pack2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
+    r = fma2(r, f, pack2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
+    r = fma2(r, f, pack2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
+    const float2 n = unpack2(t), y = unpack2(r);
+    return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(n.x) << 23)),
+                       __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(n.y) << 23)));
 }
 STRATA_DEV uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
     uint32_t r;
@@ -371,48 +413,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kMmaWarp) {
         regs_down<64>();
-        if (warp == kMmaWarp && lane == 0) pieces([&](const Piece &p) {
-        auto tile_of = [&](int n) { return SLOTS == 2 && !p.dual ? n >> 1 : n; };  // of step n, in S n & 1
+        const uint32_t me = elected();
+        if (warp == kMmaWarp) pieces([&](const Piece &p) {
             // ------------------------------------------------ matrix products
             constexpr uint32_t idesc_s = umma_idesc_f16(128, TK), idesc_o = umma_idesc_f16(128, D) | (1u << 16);
+            const bool pairs = SLOTS == 2 && !uniform(p.dual);  // two steps for each key tile
+            const int steps = uniform(p.steps);
+            const uint32_t tc = uniform(p.tc), sc[2] = {(uint32_t)uniform(p.sc[0]), (uint32_t)uniform(p.sc[1])};
             // the rows are there, and what the last piece left in tensor memory has been read
-            bool ok = mbar_wait(&qfull, p.count & 1, nullptr, &s_abort);
+            bool ok = warp_wait(&qfull, p.count & 1, &s_abort);
             tc_fence_after();
-            uint32_t s_n[2] = {p.sc[0], p.sc[1]};
             auto product_s = [&](int n) {
-                const uint32_t c = p.tc + tile_of(n), i = n & 1;
-                if (!mbar_wait(&kfull[c & 1], (c >> 1) & 1, nullptr, &s_abort)) return false;
+                const uint32_t c = tc + (pairs ? n >> 1 : n), i = n & 1;
+                if (!warp_wait(&kfull[c & 1], (c >> 1) & 1, &s_abort)) return false;
                 tc_fence_after();
-                const uint64_t qd = umma_desc_sw128(sq + (SLOTS == 2 && !p.dual ? i : 0) * C::Q);
-                const uint64_t kd = umma_desc_sw128(sk + (c & 1) * C::KV);
+                const uint64_t qd = umma_desc_sw128(sq + (pairs ? i : 0) * C::Q), kd = umma_desc_sw128(sk + (c & 1) * C::KV);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_f16(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
-                             kd + (k >> 2) * (TK * 128 / 16) + (k & 3) * 2, idesc_s, k ? 1u : 0u);
-                umma_commit(&sfull[i]);
-                if (SLOTS == 1 || p.dual || i) umma_commit(&kempty[c & 1]);
+                    umma_ss(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
+                            kd + (k >> 2) * (TK * 128 / 16) + (k & 3) * 2, idesc_s, k ? 1u : 0u, me);
+                umma_done(&sfull[i], me);
+                if (!pairs || i) umma_done(&kempty[c & 1], me);
                 return true;
             };
-            for (int n = 0; n < 2 && n < p.steps && ok; ++n) ok = product_s(n);
-            for (int n = 0; n < p.steps && ok; ++n) {
-                const uint32_t c = p.tc + tile_of(n), i = n & 1;
-                ok = mbar_wait(&vfull[c & 1], (c >> 1) & 1, nullptr, &s_abort) &&
-                     mbar_wait(&pready[i], s_n[i] & 1, nullptr, &s_abort);
+            for (int n = 0; n < 2 && n < steps && ok; ++n) ok = product_s(n);
+            for (int n = 0; n < steps && ok; ++n) {
+                const uint32_t c = tc + (pairs ? n >> 1 : n), i = n & 1;
+                ok = warp_wait(&vfull[c & 1], (c >> 1) & 1, &s_abort) &&
+                     warp_wait(&pready[i], (sc[i] + (n >> 1)) & 1, &s_abort);
                 if (!ok) break;
-                ++s_n[i];
                 tc_fence_after();
                 const uint64_t vd = umma_desc_sw128_mn(sv + (c & 1) * C::KV, TK * 128);
-                const bool fresh = SLOTS == 2 ? n < 2 : n == 0;
+                const uint32_t more = (SLOTS == 2 ? n >= 2 : n >= 1) ? 1u : 0u;
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k)
                     umma_ts(tbase + C::O_COL + (SLOTS == 2 ? i * D : 0), tbase + i * C::S_STEP + k * 8,
-                            vd + k * (2048 / 16), idesc_o, fresh && k == 0 ? 0u : 1u);
-                if (SLOTS == 1) umma_commit(&pvdone);
-                if (SLOTS == 1 || p.dual || i) umma_commit(&vempty[c & 1]);
-                if (n + 2 < p.steps) ok = product_s(n + 2);
+                            vd + k * (2048 / 16), idesc_o, k ? 1u : more, me);
+                if (SLOTS == 1) umma_done(&pvdone, me);
+                if (!pairs || i) umma_done(&vempty[c & 1], me);
+                if (n + 2 < steps) ok = product_s(n + 2);
             }
-            umma_commit(&odone);
-            mbar_wait(&odone, p.count & 1, nullptr, nullptr);  // before anything is torn down
+            umma_done(&odone, me);
+            warp_wait(&odone, p.count & 1, nullptr);  // before anything is torn down
             return ok;
         });
     } else if (warp >= 8) {
@@ -497,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 find(jj + 2);
                 uint64_t *full = is_v ? &vfull[c & 1] : &kfull[c & 1], *empty = is_v ? &vempty[c & 1] : &kempty[c & 1];
                 if (!warp_wait(empty, ((c >> 1) & 1) ^ 1, &s_abort)) return false;
-                uint8_t *to = (is_v ? sv : sk) + (c & 1) * C::KV;
+                const uint32_t to = smem_u32((is_v ? sv : sk) + (c & 1) * C::KV) + row * 128 + ((row & 7) << 4);  // chunk 0
                 if (slow) {
                     const __half2 mul = bits_h2((uint32_t)(15 - e) * 0x04000400u);  // 2^-e, -15 <= e <= 14
 #pragma unroll
@@ -516,7 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o.y = h2_bits(__hmul2(__hadd2(bits_h2(and_or(x, 0x00f000f0u, 0x54005400u)), off64), sc2));
                         o.z = h2_bits(__hmul2(__hadd2(bits_h2(and_or(y, 0x000f000fu, 0x64006400u)), off), sc2));
                         o.w = h2_bits(__hmul2(__hadd2(bits_h2(and_or(y, 0x00f000f0u, 0x54005400u)), off64), sc2));
-                        *reinterpret_cast<uint4 *>(to + sw_chunk(TK, row, (part * C::NW + i) * 4 + j)) = o;
+                        const int ch = i * 4 + j;  // of this thread's; a part is whole blocks of 64 values
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         (to ^ ((ch & 7) << 4)) + (ch >> 3) * (TK * 128) + part * (C::NW / 2) * (TK * 128)),
+                                     "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
+                                     : "memory");
                     }
                 }
                 fence_proxy_async_smem();
@@ -663,8 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t y[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float2 z = unpack2(fma2(pack2(x[e], x[e + 1]), f2, m2));
-                        x[e] = ex2(z.x), x[e + 1] = ex2(z.y);
+                        const uint64_t z2 = fma2(pack2(x[e], x[e + 1]), f2, m2);
+                        const float2 z = unpack2(z2);
+                        const float2 y2 = e / 2 % 8 < kPoly ? ex2_pair(z2) : make_float2(ex2(z.x), ex2(z.y));
+                        x[e] = y2.x, x[e + 1] = y2.y;
                         y[e / 2] = h2_bits(__floats2half2_rn(x[e], x[e + 1]));
                     }
                     tmem_st16(scol + 16 * g, y);
@@ -683,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the next chunk comes up meanwhile
                     float xa[32], xb[32];
                     tmem_ld32(scol, xa);
-#pragma unroll
+#pragma unroll 1
                     for (int g = 0; g < TK / 32; g += 2) {
                         tmem_ld_wait();
                         tmem_ld32(scol + 32 * g + 32, xb);
