@@ -33,7 +33,6 @@ namespace {
 
 constexpr int kThreads = 20 * 32;  // the last three warps only complete a group of four
 constexpr int kMmaWarp = 16;
-constexpr int kPoly = 3;  // of 8 exponentials, by polynomial
 constexpr int kInfo = 4;  // tiles whose flags are kept
 
 template <int D>
@@ -161,23 +160,6 @@ STRATA_DEV uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-// 2^z of two numbers up to 127 on the fused multiply-add units, for a share of
-// the exponentials: z = n + f with n the nearest integer, 2^f by a polynomial
-// of degree 4 (Remez' minimax in the relative error, 2^-18.5), n into the
-// exponent. Below 2^-126 the result is a number near 2^-126.
-STRATA_DEV float2 ex2_pair(uint64_t z2) {
-    float2 z = unpack2(z2);
-    z2 = pack2(fmaxf(z.x, -126.f), fmaxf(z.y, -126.f));
-    const uint64_t t = add2(z2, pack2(12582912.f, 12582912.f));  // 1.5 * 2^23: the sum's last bits are n
-    const uint64_t f = fma2(add2(t, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), z2);
-    uint64_t r = fma2(f, pack2(0x1.3997d6p-7f, 0x1.3997d6p-7f), pack2(0x1.ca1444p-5f, 0x1.ca1444p-5f));
-    r = fma2(r, f, pack2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
-    r = fma2(r, f, pack2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
-    r = fma2(r, f, pack2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
-    const float2 n = unpack2(t), y = unpack2(r);
-    return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(n.x) << 23)),
-                       __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(n.y) << 23)));
 }
 STRATA_DEV uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
     uint32_t r;
@@ -650,6 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n_s[i];
                 tc_fence_after();
                 const uint32_t scol = lanes + i * C::S_STEP;
+                float xa[32], xb[32];
+                tmem_ld32(scol, xa);
                 uint32_t slow = 0, any = 0;
 #pragma unroll
                 for (int g = 0; g < TK / 32; ++g) {
@@ -703,34 +687,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                 };
-                // weights of 32 scores, P into columns that were read before
-                auto weigh = [&](float (&x)[32], int g, float fg) {
+                // weights of 32 scores, and P of them
+                auto weigh = [&](float (&x)[32], uint32_t (&y)[16], float fg) {
                     const uint64_t f2 = pack2(fg, fg), m2 = pack2(-M, -M);
-                    uint32_t y[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const uint64_t z2 = fma2(pack2(x[e], x[e + 1]), f2, m2);
-                        const float2 z = unpack2(z2);
-                        const float2 y2 = e / 2 % 8 < kPoly ? ex2_pair(z2) : make_float2(ex2(z.x), ex2(z.y));
-                        x[e] = y2.x, x[e + 1] = y2.y;
+                        const float2 z = unpack2(fma2(pack2(x[e], x[e + 1]), f2, m2));
+                        x[e] = ex2(z.x), x[e + 1] = ex2(z.y);
                         y[e / 2] = h2_bits(__floats2half2_rn(x[e], x[e + 1]));
                     }
-                    tmem_st16(scol + 16 * g, y);
                 };
                 auto add = [&](const float (&x)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) sum[e / 2 & 1] = add2(sum[e / 2 & 1], pack2(x[e], x[e + 1]));
                 };
                 if (plain && slow == 0) {
+                    // the weights themselves tell, as fp16, whether M has to move first
                     auto chunk = [&](float (&x)[32], int g) {
-                        const float top = largest(x) * fac;
-                        if (__any_sync(kFullMask, top > M + 11.f)) move(top, g);
-                        weigh(x, g, fac);
+                        uint32_t y[16];
+                        weigh(x, y, fac);
+                        __half2 t[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            t[k] = __hmax2(__hmax2(bits_h2(y[4 * k]), bits_h2(y[4 * k + 1])),
+                                           __hmax2(bits_h2(y[4 * k + 2]), bits_h2(y[4 * k + 3])));
+                        const uint32_t m = h2_bits(__hmax2(__hmax2(t[0], t[1]), __hmax2(t[2], t[3])));
+                        if (__any_sync(kFullMask, max(m >> 16, m & 0xffffu) > 0x6800u)) {  // 2^11
+                            tmem_ld32(scol + 32 * g, x);
+                            tmem_ld_wait();
+                            move(largest(x) * fac, g);
+                            weigh(x, y, fac);
+                        }
+                        // P lies in columns that were read before
+                        tmem_st16(scol + 16 * g, y);
                         add(x);
                     };
                     // the next chunk comes up meanwhile
-                    float xa[32], xb[32];
-                    tmem_ld32(scol, xa);
 #pragma unroll 1
                     for (int g = 0; g < TK / 32; g += 2) {
                         tmem_ld_wait();
@@ -741,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         chunk(xb, g + 1);
                     }
                 } else {
+                    tmem_ld_wait();
 #pragma unroll 1
                     for (int g = 0; g < TK / 32; ++g) {
                         float x[32];
@@ -760,7 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (c0 + e > hi || c0 + e <= lo || (hole >> e & 1)) x[e] = -INFINITY;
                         const float top = largest(x) * fg;
                         if (__any_sync(kFullMask, top > M + 11.f)) move(top, g);
-                        weigh(x, g, fg);
+                        uint32_t y[16];
+                        weigh(x, y, fg);
+                        tmem_st16(scol + 16 * g, y);
                         if (own) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) x[e] *= vinv[info * TK + 32 * g + e];
