@@ -46,13 +46,13 @@ __device__ __forceinline__ float2 rope_cs(const RopeTable &t, int i, int positio
     return make_float2((float)(c * t.m), (float)(s * t.m));
 }
 
-// the same in fp32, for a result that is not rounded to fixed bits: the exact
-// fraction of a turn, rounded to fp32, then two fp32 ulp of sincospif
+// the same in fp32, for a result that is not rounded to fixed bits: 32 bits of
+// the turn's fraction, then the hardware's sine and cosine (off by 2^-20.9 at
+// most in [-pi, pi]; the row is rounded to fp16, 2^-11, next)
 __device__ __forceinline__ float2 rope_cs_f32(const RopeTable &t, int i, int position) {
-    const float x = (float)(int64_t)((uint64_t)(int64_t)position * t.freq[i]) * 0x1p-63f;
-    float s, c;
-    sincospif(x, &s, &c);
-    return make_float2(c * (float)t.m, s * (float)t.m);
+    const int32_t turn = (int32_t)((uint64_t)((int64_t)position * (int64_t)t.freq[i]) >> 32);
+    const float x = (float)turn * 0x1.921fb6p-30f;  // pi 2^-31 a unit
+    return make_float2(__cosf(x) * (float)t.m, __sinf(x) * (float)t.m);
 }
 
 // u c - v s and v c + u s, each product and each sum rounded once
@@ -155,8 +155,8 @@ struct QueryRow {
                     r.y[j / 2] |= (uint32_t)__bfloat16_as_ushort(x[rope_partner(t, i + j)]) << (16 * (j & 1));
         }
     }
-    static __device__ __forceinline__ void turn(float (&v)[P], const Raw &r, const float2 (&cs)[P], const RopeTable &t,
-                                                float scale, int lane) {
+    static __device__ __forceinline__ void rotate(float (&v)[P], const Raw &r, const float2 (&cs)[P], const RopeTable &t,
+                                                  int lane) {
         float x[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) x[j] = (j & 1) ? bf16_hi(r.x[j / 2]) : bf16_lo(r.x[j / 2]);
@@ -165,6 +165,10 @@ struct QueryRow {
             const float y = t.half ? ((j & 1) ? bf16_hi(r.y[j / 2]) : bf16_lo(r.y[j / 2])) : x[j ^ 1];
             v[j] = lane * P + j < t.rd ? fmaf(y, cs[j].y, x[j] * cs[j].x) : x[j];
         }
+    }
+    static __device__ __forceinline__ void turn(float (&v)[P], const Raw &r, const float2 (&cs)[P], const RopeTable &t,
+                                                float scale, int lane) {
+        rotate(v, r, cs, t, lane);
         fwht_warp<D>(v, lane);
 #pragma unroll
         for (int j = 0; j < P; ++j) v[j] *= rsqrt_dim<D>() * scale;

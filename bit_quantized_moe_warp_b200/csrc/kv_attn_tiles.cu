@@ -135,7 +135,7 @@ STRATA_DEV uint64_t umma_desc_sw128_mn(const void *tile, uint32_t block) {
 }
 
 // Registers of a group of four warps. 640 threads at 96 each are 480 for every
-// four-warp column; afterwards 2 x 128 + 2 x 80 + 64 = 480.
+// four-warp column; afterwards 2 x 136 + 2 x 72 + 64 = 480.
 template <int N>
 STRATA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t idesc_s = umma_idesc_f16(128, TK), idesc_o = umma_idesc_f16(128, D) | (1u << 16);
             const bool pairs = SLOTS == 2 && !uniform(p.dual);  // two steps for each key tile
             const int steps = uniform(p.steps);
+            const bool shifted = uniform(p.dual && p.it.rows <= 64);
             const uint32_t tc = uniform(p.tc), sc[2] = {(uint32_t)uniform(p.sc[0]), (uint32_t)uniform(p.sc[1])};
             // the rows are there, and what the last piece left in tensor memory has been read
             bool ok = warp_wait(&qfull, p.count & 1, &s_abort);
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t c = tc + (pairs ? n >> 1 : n), i = n & 1;
                 if (!warp_wait(&kfull[c & 1], (c >> 1) & 1, &s_abort)) return false;
                 tc_fence_after();
-                const uint64_t qd = umma_desc_sw128(sq + (pairs ? i : 0) * C::Q), kd = umma_desc_sw128(sk + (c & 1) * C::KV);
+                const uint64_t qd = umma_desc_sw128(sq + (pairs || shifted ? i : 0) * C::Q), kd = umma_desc_sw128(sk + (c & 1) * C::KV);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     umma_ss(tbase + i * C::S_STEP, qd + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         });
     } else if (warp >= 8) {
-        regs_down<80>();
+        regs_down<72>();
         pieces([&](const Piece &p) {
             // ------------------------------------------------ expanding keys (warps 8-11) and values (12-15)
             const bool is_v = warp >= 12;
@@ -528,10 +529,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < C::NW; ++i) cs[i] = h2_bits(__hmul2(bits_h2(cs[i]), mul));
                 }
                 const __half2 off = __floats2half2_rn(-1032.f, -1032.f), off64 = __floats2half2_rn(-72.f, -72.f);
-#pragma unroll
+                // a block of 32 values at a time, in one piece of code: the roles share the
+                // instruction cache
+#pragma unroll 1
                 for (int i = 0; i < C::NW; ++i) {
-                    const uint32_t words[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
-                    const __half2 sc2 = bits_h2(cs[i]);
+                    const uint32_t words[4] = {cw[0].x, cw[0].y, cw[0].z, cw[0].w};
+                    const __half2 sc2 = bits_h2(cs[0]);
+                    const uint32_t at = (to ^ ((i & 1) << 6)) + (part * (C::NW / 2) + (i >> 1)) * (TK * 128);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t x = words[j], y = x >> 8;
@@ -540,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o.y = h2_bits(__hmul2(__hadd2(bits_h2(and_or(x, 0x00f000f0u, 0x54005400u)), off64), sc2));
                         o.z = h2_bits(__hmul2(__hadd2(bits_h2(and_or(y, 0x000f000fu, 0x64006400u)), off), sc2));
                         o.w = h2_bits(__hmul2(__hadd2(bits_h2(and_or(y, 0x00f000f0u, 0x54005400u)), off64), sc2));
-                        const int ch = i * 4 + j;  // of this thread's; a part is whole blocks of 64 values
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         (to ^ ((ch & 7) << 4)) + (ch >> 3) * (TK * 128) + part * (C::NW / 2) * (TK * 128)),
-                                     "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (j << 4)), "r"(o.x), "r"(o.y),
+                                     "r"(o.z), "r"(o.w)
                                      : "memory");
                     }
+#pragma unroll
+                    for (int k = 0; k + 1 < C::NW; ++k) cw[k] = cw[k + 1], cs[k] = cs[k + 1];
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -554,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         });
     } else {
-        regs_up<128>();
+        regs_up<136>();
         pieces([&](const Piece &p) {
         auto tile_of = [&](int n) { return SLOTS == 2 && !p.dual ? n >> 1 : n; };  // of step n, in S n & 1
             // ------------------------------------------------ softmax: S slot (warps 0-3, 4-7), a thread per row
@@ -562,46 +566,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             // takes rows in a run, which share a token's angles
             {
                 using Q = QueryRow<D>;
-                constexpr int BATCH = D == 256 ? 4 : 8;
+                const int shift = p.dual && p.it.rows <= 64 ? 64 : 0;
+                constexpr int BATCH = 2;
                 const int run = (min(p.it.rows, p.dual || SLOTS == 1 ? 128 : 256) + 7) / 8;  // 32 at most
                 const int end = min(warp * run + run, p.it.rows);
-                auto tok_of = [&](int r) { return p.s.t0 + by_group(a, p.it.row0 + min(r, p.it.rows - 1)); };
+                auto tok_of = [&](int r) { return p.s.t0 + by_group(a, p.it.row0 + min(max(r, 0), p.it.rows - 1)); };
                 const int pos_lane = tab.rd ? a.positions[tok_of(warp * run + lane)] : 0;
                 float2 cs[P];
                 int64_t at = -1;
-                for (int r0 = warp * run; r0 < end; r0 += BATCH) {
-                    typename Q::Raw raw[BATCH];
+                typename Q::Raw raw[BATCH], next[BATCH];
+                auto fetch = [&](int r0) {
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {
                         const int row = p.it.row0 + min(r0 + k, p.it.rows - 1), i = by_group(a, row);
-                        Q::load(raw[k], a.q + (p.s.t0 + i) * a.d.q_token_stride + (int64_t)(p.hk * a.group + row - i * a.group) * D,
+                        Q::load(next[k], a.q + (p.s.t0 + i) * a.d.q_token_stride + (int64_t)(p.hk * a.group + row - i * a.group) * D,
                                 tab, lane);
                     }
+                };
+                fetch(warp * run);
+#pragma unroll 1
+                for (int r0 = warp * run; r0 < end; r0 += BATCH) {
 #pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        const int r = r0 + k;
-                        if (r >= end) break;  // what lies behind keeps older rows' values: finite, never stored
+                    for (int k = 0; k < BATCH; ++k) raw[k] = next[k];
+                    fetch(r0 + BATCH);
+                    float q[BATCH][P], m[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {  // past the end: the last row once more
+                        const int r = min(r0 + k, end - 1);
                         if (tok_of(r) != at) {
                             at = tok_of(r);
                             Q::angles(cs, tab, __shfl_sync(kFullMask, pos_lane, r - warp * run), lane);
                         }
-                        float q[P], m = 0.f;
-                        Q::turn(q, raw[k], cs, tab, a.scale_log2 < 0.f ? -1.f : 1.f, lane);
+                        Q::rotate(q[k], raw[k], cs, tab, lane);
+                    }
 #pragma unroll
-                        for (int i = 0; i < P; ++i) m = fmaxf(m, fabsf(q[i]));
+                    for (int k = 0; k < BATCH; ++k) {
+                        fwht_warp<D>(q[k], lane);
+                        m[k] = 0.f;
 #pragma unroll
-                        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-                        const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 252u);
-                        const float mul = m > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
+                        for (int i = 0; i < P; ++i) {
+                            q[k][i] *= a.scale_log2 < 0.f ? -rsqrt_dim<D>() : rsqrt_dim<D>();
+                            m[k] = fmaxf(m[k], fabsf(q[k][i]));
+                        }
+                    }
+#pragma unroll
+                    for (int x = 16; x; x >>= 1)
+#pragma unroll
+                        for (int k = 0; k < BATCH; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(kFullMask, m[k], x));
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int r = r0 + k;
+                        if (r >= end) break;  // what lies behind keeps older rows' values: never stored
+                        const uint32_t ex = min(max(__float_as_uint(m[k]) >> 23, 1u), 252u);
+                        const float mul = m[k] > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
 #pragma unroll
                         for (int i = 0; i < P; ++i) {
                             const int d = lane * P + i;
+                            const __half x = __float2half_rn(q[k][i] * mul);
                             *reinterpret_cast<__half *>(sq + (r >> 7) * C::Q + sw_chunk(128, r & 127, d >> 3) +
-                                                        place_of(d & 7) * 2) = __float2half_rn(q[i] * mul);
+                                                        place_of(d & 7) * 2) = x;
+                            if (shift)
+                                *reinterpret_cast<__half *>(sq + C::Q + sw_chunk(128, r + 64, d >> 3) + place_of(d & 7) * 2) = x;
                         }
                         // above zero, so that a masked score stays -inf
                         if (lane == 0)
-                            sfac[r] = fmaxf(fabsf(a.scale_log2) * (m > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
+                            sfac[r] = fmaxf(fabsf(a.scale_log2) * (m[k] > 0.f ? __uint_as_float((ex + 1) << 23) : 1.f), 1e-37f);
                     }
                 }
                 fence_proxy_async_smem();
@@ -613,13 +642,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = warp >> 2, tr = threadIdx.x & 127;
             const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
             const uint32_t ocol = lanes + C::O_COL + (SLOTS == 2 ? slot * D : 0);
-            const int r = (SLOTS == 2 && !p.dual ? slot * 128 : 0) + tr;  // of the item
+            // At most 64 rows against alternate tiles: the second S has them in the
+            // other half of tensor memory, for the warps of the other two schedulers.
+            const int shift = p.dual && p.it.rows <= 64 ? 64 * slot : 0;
+            const int r = (SLOTS == 2 && !p.dual ? slot * 128 : 0) + tr - shift;  // of the item; outside it: no row
+            const bool busy = __any_sync(kFullMask, r >= 0 && r < p.it.rows);
             const int pos = p.s.L - p.s.n + by_group(a, p.it.row0 + min(r, p.it.rows - 1));
             const int hi = min(pos, p.s.L - 1), lo = a.d.window > 0 ? (int)max((int64_t)pos - a.d.window, (int64_t)-1) : -1;
             const int full_hi = p.s.L - p.s.n + by_group(a, p.it.row0);
             const int full_lo =
                 a.d.window > 0 ? (int)max((int64_t)p.s.L - p.s.n + by_group(a, p.it.row0 + p.it.rows - 1) - a.d.window, (int64_t)-1) : -1;
-            const float fac = sfac[r];
+            const float fac = sfac[max(r, 0)];
             float M = -FLT_MAX, l = 0.f;
             uint32_t n_s[2] = {p.sc[0], p.sc[1]};
             bool ok = true;
@@ -630,9 +663,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_wait(&sfull[i], n_s[i] & 1, &s_abort);
                 if (!ok) break;
                 ++n_s[i];
+                if (!busy) {  // P of rows that are not there may be anything
+                    if (lane == 0) mbar_arrive(&pready[i]);
+                    continue;
+                }
                 tc_fence_after();
                 const uint32_t scol = lanes + i * C::S_STEP;
-                float xa[32], xb[32];
+                float xa[32];
                 tmem_ld32(scol, xa);
                 uint32_t slow = 0, any = 0;
 #pragma unroll
@@ -687,15 +724,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                 };
-                // weights of 32 scores, and P of them
-                auto weigh = [&](float (&x)[32], uint32_t (&y)[16], float fg) {
+                auto weigh = [&](const float (&x)[32], float (&w)[32], float fg) {
                     const uint64_t f2 = pack2(fg, fg), m2 = pack2(-M, -M);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 z = unpack2(fma2(pack2(x[e], x[e + 1]), f2, m2));
-                        x[e] = ex2(z.x), x[e + 1] = ex2(z.y);
-                        y[e / 2] = h2_bits(__floats2half2_rn(x[e], x[e + 1]));
+                        w[e] = ex2(z.x), w[e + 1] = ex2(z.y);
                     }
+                };
+                auto pack = [&](const float (&w)[32], uint32_t (&y)[16]) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] = h2_bits(__floats2half2_rn(w[2 * e], w[2 * e + 1]));
                 };
                 auto add = [&](const float (&x)[32]) {
 #pragma unroll
@@ -703,9 +742,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (plain && slow == 0) {
                     // the weights themselves tell, as fp16, whether M has to move first
-                    auto chunk = [&](float (&x)[32], int g) {
+#pragma unroll 1
+                    for (int g = 0; g < TK / 32; ++g) {
+                        float w[32];
                         uint32_t y[16];
-                        weigh(x, y, fac);
+                        tmem_ld_wait();
+                        weigh(xa, w, fac);
+                        if (g + 1 < TK / 32) tmem_ld32(scol + 32 * g + 32, xa);  // comes up meanwhile
+                        pack(w, y);
                         __half2 t[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -713,24 +757,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            __hmax2(bits_h2(y[4 * k + 2]), bits_h2(y[4 * k + 3])));
                         const uint32_t m = h2_bits(__hmax2(__hmax2(t[0], t[1]), __hmax2(t[2], t[3])));
                         if (__any_sync(kFullMask, max(m >> 16, m & 0xffffu) > 0x6800u)) {  // 2^11
-                            tmem_ld32(scol + 32 * g, x);
+                            tmem_ld32(scol + 32 * g, w);
                             tmem_ld_wait();
-                            move(largest(x) * fac, g);
-                            weigh(x, y, fac);
+                            move(largest(w) * fac, g);
+                            weigh(w, w, fac);
+                            pack(w, y);
                         }
-                        // P lies in columns that were read before
-                        tmem_st16(scol + 16 * g, y);
-                        add(x);
-                    };
-                    // the next chunk comes up meanwhile
-#pragma unroll 1
-                    for (int g = 0; g < TK / 32; g += 2) {
-                        tmem_ld_wait();
-                        tmem_ld32(scol + 32 * g + 32, xb);
-                        chunk(xa, g);
-                        tmem_ld_wait();
-                        if (g + 2 < TK / 32) tmem_ld32(scol + 32 * g + 64, xa);
-                        chunk(xb, g + 1);
+                        tmem_st16(scol + 16 * g, y);  // columns that were read before
+                        add(w);
                     }
                 } else {
                     tmem_ld_wait();
@@ -754,7 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float top = largest(x) * fg;
                         if (__any_sync(kFullMask, top > M + 11.f)) move(top, g);
                         uint32_t y[16];
-                        weigh(x, y, fg);
+                        weigh(x, x, fg);
+                        pack(x, y);
                         tmem_st16(scol + 16 * g, y);
                         if (own) {
 #pragma unroll
@@ -774,18 +809,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(&odone, p.count & 1, &s_abort) && ok;  // the next piece's rows overwrite these, too
             if (slot < SLOTS) {
                 tc_fence_after();
-                float *other = reinterpret_cast<float *>(sk);  // the second O of a p.dual item: [D][128 rows]
+                float *other = reinterpret_cast<float *>(sk);  // the second O of a dual item: [D][128 rows]
                 float f0 = 1.f, f1 = 0.f;
                 if (p.dual) {
-                    if (slot == 1) {
-                        sml[tr] = make_float2(M, mine ? l : 0.f);
+                    if (slot == 1 && busy) {
+                        sml[r] = make_float2(M, mine ? l : 0.f);
 #pragma unroll 1
                         for (int g = 0; g < D / 16 && mine; ++g) {
                             float x[16];
                             tmem_ld16(ocol + 16 * g, x);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) other[(16 * g + e) * 128 + tr] = x[e];
+                            for (int e = 0; e < 16; ++e) other[(16 * g + e) * 128 + r] = x[e];
                         }
                     }
                     named_barrier(1, 256);
@@ -801,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float bad = ok && !*(volatile int *)&s_abort ? 1.f : NAN;
                 const float norm = p.whole ? bad * (l > 0.f ? rsqrt_dim<D>() / l : 0.f) : bad;
                 f0 *= norm, f1 *= norm;
-                if (!p.dual || slot == 0) {
+                if ((!p.dual || slot == 0) && busy) {
                     auto row16 = [&](float (&x)[16], int col) {  // 16 columns, values in order
                         float y[16];
                         tmem_ld16(ocol + col, y);
@@ -809,32 +844,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float z = mine ? y[e] * f0 : 0.f;
-                            if (p.dual && p.nt > 1) z = fmaf(other[(col + e) * 128 + tr], f1, z);
+                            if (p.dual && p.nt > 1) z = fmaf(other[(col + e) * 128 + r], f1, z);
                             x[(e & 8) + value_at(e & 7)] = z;
                         }
                     };
                     if (p.whole) {
                         const int i = by_group(a, p.it.row0 + r), h = p.hk * a.group + p.it.row0 + r - i * a.group;
                         __nv_bfloat16 *dst = a.out + (p.s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
-                        // H of D = H of D / 64 over H of 64: one 64-value output block at a time
+                        // H of D = H of D / 16 over H of 16: 16 values of the result at a time
 #pragma unroll 1
-                        for (int q = 0; q < D / 64; ++q) {
-                            float x[64];
+                        for (int q = 0; q < D / 16; ++q) {
+                            float x[16];
 #pragma unroll
-                            for (int j = 0; j < D / 64; ++j) {
+                            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+#pragma unroll 2
+                            for (int j = 0; j < D / 16; ++j) {
                                 const float sg = __popc(j & q) & 1 ? -1.f : 1.f;
+                                float y[16];
+                                row16(y, 16 * j);
 #pragma unroll
-                                for (int g = 0; g < 4; ++g) {
-                                    float y[16];
-                                    row16(y, 64 * j + 16 * g);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) x[16 * g + e] = j ? fmaf(sg, y[e], x[16 * g + e]) : y[e];
-                                }
+                                for (int e = 0; e < 16; ++e) x[e] = fmaf(sg, y[e], x[e]);
                             }
 #pragma unroll
-                            for (int d = 1; d < 64; d <<= 1)
+                            for (int d = 1; d < 16; d <<= 1)
 #pragma unroll
-                                for (int e = 0; e < 64; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     if (!(e & d)) {
                                         const float y = x[e], z = x[e + d];
                                         x[e] = y + z;
@@ -842,8 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     }
                             if (store) {
 #pragma unroll
-                                for (int e = 0; e < 64; e += 8)
-                                    *reinterpret_cast<uint4 *>(dst + 64 * q + e) =
+                                for (int e = 0; e < 16; e += 8)
+                                    *reinterpret_cast<uint4 *>(dst + 16 * q + e) =
                                         make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
                                                    pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
                             }
