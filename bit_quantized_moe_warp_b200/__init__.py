@@ -140,10 +140,13 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if device is None:
+            return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without building a Stream
+        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -153,13 +156,25 @@ def _host_i32(v):
     """A host list of int32 as a CPU tensor (which keeps its memory) and its length."""
     import torch
     t = v if isinstance(v, torch.Tensor) else torch.as_tensor(v)
-    if t.device.type != "cpu" or t.dim() != 1 or (t.numel() and (t.is_floating_point() or t.is_complex())):
+    if t.get_device() >= 0 or t.dim() != 1 or (t.numel() and (t.is_floating_point() or t.is_complex())):
         raise ValueError("page lists are one-dimensional host arrays of whole numbers")
     if t.dtype != torch.int32 or not t.is_contiguous():
         if t.numel() and (int(t.max()) > 0x7fffffff or int(t.min()) < -0x80000000):
             raise ValueError("page numbers are int32")
         t = t.to(torch.int32).contiguous()
     return t, t.numel()
+
+
+def _on(device, call, *args):
+    """call(*args) with GPU `device` (an index) current; a status that is not OK raises."""
+    import torch
+    if torch.cuda.current_device() == device:
+        status = call(*args)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args)
+    if status != STRATA_OK:
+        _check(status)
 
 
 def _check(status: int):
@@ -441,12 +456,12 @@ class MoELayer:
         strata_moe_pack_expert_device(self.desc, gc, gs, uc, us, dc, ds, dst, stream)
 
 
-def _need(t, name, dtype, device=None):
-    """The entry points take raw pointers: refuse a tensor of another type or device than they will read."""
-    if t.dtype != dtype:
+def _need(t, name, dtype, device):
+    """The entry points take raw pointers: refuse a tensor of another type or device (an index) than they will read."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} is on {t.device}, not on {device if device is not None else 'a GPU'}")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} is on {t.device}, not on {f'GPU {device}' if device >= 0 else 'a GPU'}")
 
 
 class Rope:
@@ -482,18 +497,18 @@ class Rope:
         n, heads, D = x.shape
         if out is None:
             out = torch.empty((n, heads, D), dtype=x.dtype, device=x.device)
-        dev = x.device
-        _need(x, "x", torch.bfloat16)
+        dev = x.get_device()
+        _need(x, "x", torch.bfloat16, dev)
         _need(out, "out", torch.bfloat16, dev)
         _need(positions, "positions", torch.int32, dev)
         if D != self.head_dim or out.shape != x.shape or positions.shape != (n,):
             raise ValueError(f"x {tuple(x.shape)}, out {tuple(out.shape)}, positions {tuple(positions.shape)}, "
                              f"head_dim {self.head_dim}")
-        if x.stride(2) != 1 or out.stride(2) != 1 or not positions.is_contiguous():
+        (xt, xh, x1), (ot, oh, o1) = x.stride(), out.stride()
+        if x1 != 1 or o1 != 1 or not positions.is_contiguous():
             raise ValueError("the values of a row and the positions must be contiguous")
-        with torch.cuda.device(dev):
-            strata_rope_apply(self.handle, x, x.stride(0), x.stride(1), positions, n, heads, out, out.stride(0),
-                              out.stride(1), stream)
+        _on(dev, _lib.strata_rope_apply, self.handle, x.data_ptr(), xt, xh, positions.data_ptr(), n, heads,
+            out.data_ptr(), ot, oh, _stream(stream, dev))
         return out
 
 
@@ -504,17 +519,18 @@ class Kv4Cache:
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         import torch
         pages, heads, page, half = k_codes.shape
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         for name, t, dtype, last in (("k_codes", k_codes, torch.uint8, half), ("v_codes", v_codes, torch.uint8, half),
                                      ("k_scales", k_scales, torch.float16, half // 16),
                                      ("v_scales", v_scales, torch.float16, half // 16)):
-            _need(t, name, dtype, self.device)
+            _need(t, name, dtype, self.index)
             if tuple(t.shape) != (pages, heads, page, last) or not t.is_contiguous():
                 raise ValueError(f"{name} {tuple(t.shape)} does not fit codes {tuple(k_codes.shape)}")
         self.tensors = (k_codes, k_scales, v_codes, v_scales)
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, 2 * half
         self.desc = strata_kv4_cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, heads, page,
                                      2 * half)
+        self._desc = ctypes.addressof(self.desc)
 
     @classmethod
     def empty(cls, n_pages, page_size, n_kv_heads, head_dim, device="cuda"):
@@ -529,23 +545,25 @@ class Kv4Cache:
         slot; negative: dropped), k through `rope` at positions int32 [tokens]."""
         import torch
         n = k.shape[0]
-        D, dev = self.head_dim, self.device
+        D, dev = self.head_dim, self.index
         _need(k, "k", torch.bfloat16, dev)
         _need(v, "v", torch.bfloat16, dev)
         _need(slots, "slots", torch.int64, dev)
-        if tuple(k.shape) != (n, self.n_kv_heads, D) or v.shape != k.shape or tuple(slots.shape) != (n,):
+        if k.shape != (n, self.n_kv_heads, D) or v.shape != k.shape or slots.shape != (n,):
             raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)}, slots {tuple(slots.shape)}")
-        if n and (k.stride()[1:] != (D, 1) or v.stride()[1:] != (D, 1) or not slots.is_contiguous()):
+        (kt, kh, k1), (vt, vh, v1) = k.stride(), v.stride()
+        if n and ((kh, k1) != (D, 1) or (vh, v1) != (D, 1) or not slots.is_contiguous()):
             raise ValueError("the heads of a token and the slots must be contiguous")
+        handle = where = None
         if rope is not None:
             if positions is None:
                 raise ValueError("rope needs positions")
             _need(positions, "positions", torch.int32, dev)
-            if tuple(positions.shape) != (n,) or not positions.is_contiguous():
+            if positions.shape != (n,) or not positions.is_contiguous():
                 raise ValueError(f"positions {tuple(positions.shape)}")
-        with torch.cuda.device(dev):
-            strata_kv4_append(self.desc, None if rope is None else rope.handle, k, k.stride(0), v, v.stride(0),
-                              positions if rope is not None else None, slots, n, stream)
+            handle, where = rope.handle, positions.data_ptr()
+        _on(dev, _lib.strata_kv4_append, self._desc, handle, k.data_ptr(), kt, v.data_ptr(), vt, where, slots.data_ptr(),
+            n, _stream(stream, dev))
 
     def attention_workspace(self, n_q_heads):
         """A workspace for attention() with n_q_heads query heads, whatever the sequences."""
@@ -562,9 +580,9 @@ class Kv4Cache:
         (all int32); max_q_len its longest query run. Rows outside every sequence stay as they are in `out`."""
         import torch
         n, heads, D = q.shape
-        dev = self.device
+        dev = self.index
         if out is None:
-            out = torch.zeros((n, heads, D), dtype=q.dtype, device=dev)
+            out = torch.zeros((n, heads, D), dtype=q.dtype, device=self.device)
         _need(q, "q", torch.bfloat16, dev)
         _need(out, "out", torch.bfloat16, dev)
         for name, t in (("q_offsets", q_offsets), ("kv_lens", kv_lens), ("block_table", block_table)):
@@ -572,26 +590,30 @@ class Kv4Cache:
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         B = kv_lens.shape[0]
-        if D != self.head_dim or out.shape != q.shape or tuple(q_offsets.shape) != (B + 1,) or \
+        if D != self.head_dim or out.shape != q.shape or q_offsets.shape != (B + 1,) or \
                 block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)}, q_offsets {tuple(q_offsets.shape)}, "
                              f"kv_lens {tuple(kv_lens.shape)}, block_table {tuple(block_table.shape)}")
-        if n and (q.stride()[1:] != (D, 1) or out.stride()[1:] != (D, 1)):
+        (qt, qh, q1), (ot, oh, o1) = q.stride(), out.stride()
+        if n and ((qh, q1) != (D, 1) or (oh, o1) != (D, 1)):
             raise ValueError("the heads of a token must be contiguous")
+        handle = where = None
         if rope is not None:
             if positions is None:
                 raise ValueError("rope needs positions")
             _need(positions, "positions", torch.int32, dev)
-            if tuple(positions.shape) != (n,) or not positions.is_contiguous():
+            if positions.shape != (n,) or not positions.is_contiguous():
                 raise ValueError(f"positions {tuple(positions.shape)}")
+            handle, where = rope.handle, positions.data_ptr()
         if workspace is None:
             workspace = self.attention_workspace(heads)
-        desc = strata_kv4_attn_desc(B, heads, max_q_len, block_table.shape[1], n, q.stride(0), out.stride(0), window,
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"the workspace is on {workspace.device}, not contiguous on GPU {dev}")
+        desc = strata_kv4_attn_desc(B, heads, max_q_len, block_table.shape[1], n, qt, ot, window,
                                     D ** -0.5 if scale is None else scale)
-        with torch.cuda.device(dev):
-            strata_kv4_attention(self.desc, desc, None if rope is None else rope.handle,
-                                 positions if rope is not None else None, q, q_offsets, kv_lens, block_table, out,
-                                 workspace, workspace.numel() * workspace.element_size(), stream)
+        _on(dev, _lib.strata_kv4_attention, self._desc, ctypes.addressof(desc), handle, where, q.data_ptr(),
+            q_offsets.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(stream, dev))
         return out
 
 
@@ -606,7 +628,12 @@ class Kv4CacheSet:
 
     def copy_pages(self, src, dst, stream=None):
         """Page src[i] -> dst[i] in every cache; src and dst are host lists (see strata_kv4_copy_pages)."""
-        import torch
-        if self.caches:
-            with torch.cuda.device(self.caches[0].device):
-                strata_kv4_copy_pages(self.descs, src, dst, stream)
+        if not self.caches:
+            return
+        s, n = _host_i32(src)
+        d, m = _host_i32(dst)
+        if n != m:
+            raise ValueError(f"{n} source pages and {m} destinations")
+        dev = self.caches[0].index
+        _on(dev, _lib.strata_kv4_copy_pages, ctypes.addressof(self.descs), len(self.caches), s.data_ptr(), d.data_ptr(),
+            n, _stream(stream, dev))

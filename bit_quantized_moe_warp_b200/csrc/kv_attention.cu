@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
 template <int D, int NT>
 cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     using C = Split<D, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k_attn_split<D, NT>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     k_attn_split<D, NT><<<C::CTAS, kSplitWarps * 32, C::SMEM, st>>>(tab, a);
     return launch_join<D, C::ROWS, 8>(a, C::CTAS, st);

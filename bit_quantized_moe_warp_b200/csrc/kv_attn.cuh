@@ -3,6 +3,7 @@
 // partial results.
 #pragma once
 
+#include <atomic>
 #include <cfloat>
 #include <math.h>
 
@@ -149,6 +150,19 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
         }
         __syncthreads();
     }
+}
+
+// Dynamic shared memory of a kernel, set once for each device: done has a bit each
+template <typename Kernel>
+cudaError_t allow_smem(Kernel *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 template <int D, int ROWS, int WPR>

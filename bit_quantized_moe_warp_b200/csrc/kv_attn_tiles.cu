@@ -912,7 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     using C = Tiles<D>;
-    const cudaError_t e = cudaFuncSetAttribute(k_attn_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k_attn_tiles<D>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     k_attn_tiles<D><<<kSms, kThreads, C::SMEM, st>>>(tab, a);
     return launch_join<D, C::ROWS, 1>(a, kSms, st);

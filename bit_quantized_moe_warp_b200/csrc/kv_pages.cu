@@ -2,6 +2,7 @@
 // rotary + encoder of new rows into their slots, and copies of whole pages.
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "abi_internal.h"
 #include "kv4_row.cuh"
@@ -41,28 +42,58 @@ struct Row {
     static constexpr int kLanes = D / (8 * kRuns);
 };
 
+// two values at a time (add and fused multiply-add of pairs); a - b is
+// fma(b, -1, a), which rounds the same
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 template <int D>
 __device__ __forceinline__ void fwht_ordered(float (&x)[Row<D>::kRuns][8], int l) {
     using R = Row<D>;
+    uint64_t p[R::kRuns][4];
+    const uint64_t minus = pair_of(-1.f, -1.f);
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1)
+    for (int m = 0; m < R::kRuns; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[m][e] = pair_of(__fadd_rn(x[m][2 * e], x[m][2 * e + 1]), __fsub_rn(x[m][2 * e], x[m][2 * e + 1]));
+#pragma unroll
+    for (int s = 1; s < 4; s <<= 1)
 #pragma unroll
         for (int m = 0; m < R::kRuns; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
                 if (!(e & s)) {
-                    const float a = x[m][e], b = x[m][e + s];
-                    x[m][e] = __fadd_rn(a, b);
-                    x[m][e + s] = __fsub_rn(a, b);
+                    const uint64_t a = p[m][e], b = p[m][e + s];
+                    p[m][e] = add_pair(a, b);
+                    p[m][e + s] = fma_pair(b, minus, a);
                 }
 #pragma unroll
     for (int k = 1; k < R::kLanes; k <<= 1) {
         const float sg = (l & k) ? -1.f : 1.f;  // the upper lane forms partner - own
+        const uint64_t sg2 = pair_of(sg, sg);
 #pragma unroll
         for (int m = 0; m < R::kRuns; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[m][e] = __fmaf_rn(sg, x[m][e], __shfl_xor_sync(kFullMask, x[m][e], k));
+            for (int e = 0; e < 4; ++e) {
+                float a, b;
+                split(p[m][e], a, b);
+                const uint64_t o = pair_of(__shfl_xor_sync(kFullMask, a, k), __shfl_xor_sync(kFullMask, b, k));
+                p[m][e] = fma_pair(sg2, p[m][e], o);
+            }
     }
 #pragma unroll
     for (int s = 1; s < R::kRuns; s <<= 1)
@@ -70,11 +101,15 @@ __device__ __forceinline__ void fwht_ordered(float (&x)[Row<D>::kRuns][8], int l
         for (int m = 0; m < R::kRuns; ++m)
             if (!(m & s))
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = x[m][e], b = x[m + s][e];
-                    x[m][e] = __fadd_rn(a, b);
-                    x[m + s][e] = __fsub_rn(a, b);
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t a = p[m][e], b = p[m + s][e];
+                    p[m][e] = add_pair(a, b);
+                    p[m + s][e] = fma_pair(b, minus, a);
                 }
+#pragma unroll
+    for (int m = 0; m < R::kRuns; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split(p[m][e], x[m][2 * e], x[m][2 * e + 1]);
 }
 
 struct AppendArgs {
@@ -85,91 +120,122 @@ struct AppendArgs {
     const int64_t *slots;
     int64_t n_tokens;
     int tokens_per_block;
-    int chunked;  // rotary pairs lie in whole 8-value chunks
 };
 
+// What turns a key row: nothing, or pairs that one lane holds (the half layout
+// over the whole head: a chunk's partner is R / 2 runs on; the interleaved one),
+// or partners read once more from memory
+enum { kPlain, kHalfWhole, kInterleaved, kOther };
+
 // One block takes tokens_per_block tokens: their cosines and sines once
-// (fp64) into shared memory, then the 2 n_kv_heads rows of each.
-template <int D>
+// (fp64) into shared memory, while the first rows are on their way, then the key
+// rows and the value rows of each (in this order, so that warps agree). Bound by
+// instruction issue: 7 butterflies, rotary and rounding of every value; values
+// go in pairs where the operation has a form for two.
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__ RopeTable tab,
                                                         const __grid_constant__ AppendArgs a) {
     using R = Row<D>;
-    extern __shared__ float2 cs[];  // [tokens_per_block][rd / 2]
+    extern __shared__ __align__(16) float2 cs[];  // [tokens_per_block][rd / 2]
     const int pairs = tab.rd / 2;
     const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block;
     const int nt = (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0);
-    for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-        const int t = i / pairs;
-        cs[i] = rope_cs(tab, i - t * pairs, a.positions[t0 + t]);
-    }
-    __syncthreads();
     const int heads = a.c.n_kv_heads;
-    const int rows = nt * 2 * heads;
+    const int k_rows = nt * heads, rows = 2 * k_rows;
     const int l = threadIdx.x % R::kLanes;
     constexpr int kRowsPerPass = kThreads / R::kLanes;
+    int r = threadIdx.x / R::kLanes;
+    uint4 raw[R::kRuns];
+    int64_t slot = -1;
+    const __nv_bfloat16 *src = nullptr;
+    int t = 0, h = 0;
+    auto fetch = [&]() {
+        if (r >= rows) return;
+        const int q = r < k_rows ? r : r - k_rows;
+        t = q / heads;
+        h = q - t * heads;
+        src = (r < k_rows ? a.k + (t0 + t) * a.k_tok : a.v + (t0 + t) * a.v_tok) + (int64_t)h * D;
+#pragma unroll
+        for (int m = 0; m < R::kRuns; ++m) raw[m] = *reinterpret_cast<const uint4 *>(src + 8 * (l + R::kLanes * m));
+        slot = a.slots[t0 + t];
+    };
+    fetch();
+    if (MODE != kPlain) {
+        for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
+            const int u = i / pairs;
+            cs[i] = rope_cs(tab, i - u * pairs, a.positions[t0 + u]);
+        }
+        __syncthreads();
+    }
     for (int r0 = 0; r0 < rows; r0 += kRowsPerPass) {  // block-uniform: the shuffles need whole warps
-        const int r = r0 + threadIdx.x / R::kLanes;
-        const bool live = r < rows;
-        const int t = live ? r / (2 * heads) : 0;
-        const int kvh = r - t * 2 * heads;
-        const bool is_v = kvh >= heads;
-        const int h = is_v ? kvh - heads : kvh;
+        const bool live = r < rows, is_v = r >= k_rows;
         float x[R::kRuns][8];
-        if (live) {
-            const __nv_bfloat16 *src =
-                (is_v ? a.v + (t0 + t) * a.v_tok : a.k + (t0 + t) * a.k_tok) + (int64_t)h * D;
+#pragma unroll
+        for (int m = 0; m < R::kRuns; ++m) {
+            const uint32_t w[4] = {raw[m].x, raw[m].y, raw[m].z, raw[m].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[m][2 * j] = live ? bf16_lo(w[j]) : 0.f;
+                x[m][2 * j + 1] = live ? bf16_hi(w[j]) : 0.f;
+            }
+        }
+        if (MODE != kPlain && live && !is_v) {
             const float2 *ct = cs + t * pairs;
-            const int rd = is_v ? 0 : tab.rd;
+            if constexpr (MODE == kHalfWhole) {
 #pragma unroll
-            for (int m = 0; m < R::kRuns; ++m) {
-                const int c8 = 8 * (l + R::kLanes * m);  // first value of the chunk
-                const uint4 w4 = *reinterpret_cast<const uint4 *>(src + c8);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                for (int m = 0; m < R::kRuns / 2; ++m) {
+                    const float4 *c = reinterpret_cast<const float4 *>(ct + 8 * (l + R::kLanes * m));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[m][2 * j] = bf16_lo(w[j]);
-                    x[m][2 * j + 1] = bf16_hi(w[j]);
-                }
-                if (c8 >= rd) continue;
-                float p[8];  // rotary partners
-                if (!tab.half) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = x[m][e ^ 1];
-                } else if (a.chunked) {
-                    const uint4 q4 = *reinterpret_cast<const uint4 *>(src + (c8 < pairs ? c8 + pairs : c8 - pairs));
-                    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        p[2 * j] = bf16_lo(q[j]);
-                        p[2 * j + 1] = bf16_hi(q[j]);
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 k = c[e / 2];
+                        const float2 c0 = make_float2(k.x, k.y), c1 = make_float2(k.z, k.w);
+                        float *u = x[m] + e, *v = x[m + R::kRuns / 2] + e;
+                        const uint32_t ru = pack_bf16(rope_first(u[0], v[0], c0), rope_first(u[1], v[1], c1));
+                        const uint32_t rv = pack_bf16(rope_second(u[0], v[0], c0), rope_second(u[1], v[1], c1));
+                        u[0] = bf16_lo(ru), u[1] = bf16_hi(ru), v[0] = bf16_lo(rv), v[1] = bf16_hi(rv);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        p[e] = c8 + e < rd ? __bfloat162float(src[rope_partner(tab, c8 + e)]) : 0.f;
                 }
+            } else if constexpr (MODE == kInterleaved) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = c8 + e;
-                    if (i < rd) {
-                        const float2 c = ct[rope_pair(tab, i)];
-                        const float y = rope_is_second(tab, i) ? rope_second(p[e], x[m][e], c)
-                                                               : rope_first(x[m][e], p[e], c);
-                        x[m][e] = __bfloat162float(__float2bfloat16_rn(y));
+                for (int m = 0; m < R::kRuns; ++m) {
+                    const int c8 = 8 * (l + R::kLanes * m);
+                    if (c8 >= tab.rd) continue;
+                    const float4 *c = reinterpret_cast<const float4 *>(ct + c8 / 2);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 k = c[e / 4];
+                        const float2 c0 = make_float2(k.x, k.y), c1 = make_float2(k.z, k.w);
+                        float *u = x[m] + e;
+                        const uint32_t r0_ = pack_bf16(rope_first(u[0], u[1], c0), rope_second(u[0], u[1], c0));
+                        const uint32_t r1_ = pack_bf16(rope_first(u[2], u[3], c1), rope_second(u[2], u[3], c1));
+                        u[0] = bf16_lo(r0_), u[1] = bf16_hi(r0_), u[2] = bf16_lo(r1_), u[3] = bf16_hi(r1_);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < R::kRuns; ++m) {
+                    const int c8 = 8 * (l + R::kLanes * m);  // first value of the chunk
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = c8 + e;
+                        if (i < tab.rd) {
+                            const float p = __bfloat162float(src[rope_partner(tab, i)]);
+                            const float2 c = ct[rope_pair(tab, i)];
+                            const float y = rope_is_second(tab, i) ? rope_second(p, x[m][e], c) : rope_first(x[m][e], p, c);
+                            x[m][e] = __bfloat162float(__float2bfloat16_rn(y));
+                        }
                     }
                 }
             }
-        } else {
-#pragma unroll
-            for (int m = 0; m < R::kRuns; ++m)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[m][e] = 0.f;
         }
-        fwht_ordered<D>(x, l);
-        int64_t slot = live ? a.slots[t0 + t] : -1;
         const int64_t page = slot / a.c.page_size;
-        const bool store = slot >= 0 && page < a.c.n_pages;
+        const bool store = live && slot >= 0 && page < a.c.n_pages;
         const int64_t row = (page * heads + h) * a.c.page_size + (slot - page * a.c.page_size);
+        uint32_t *codes = static_cast<uint32_t *>(is_v ? a.c.v_codes : a.c.k_codes) + (store ? row * (D / 8) : 0);
+        __half *scales = static_cast<__half *>(is_v ? a.c.v_scales : a.c.k_scales) + (store ? row * (D / 32) : 0);
+        r += kRowsPerPass;
+        fetch();  // the next row, behind this one's arithmetic
+        fwht_ordered<D>(x, l);
 #pragma unroll
         for (int m = 0; m < R::kRuns; ++m) {
             float amax = 0.f;
@@ -183,23 +249,19 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
             const __half hs = __float2half_rn(fminf(__fdiv_rn(amax, 7.f), 65504.f));
             const float s = __half2float(hs);
             const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+            // 1.5 * 2^23 + 8 rounds the exact product to an integer, ties to even, and
+            // leaves q + 8 in the low bits; a quotient of 8 or more (tiny or saturated
+            // scales) ends at 7 like any other
             uint32_t word = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                int q;
-                if (fabsf(__fmul_rn(x[m][e], inv)) >= 8.f) {
-                    q = x[m][e] > 0.f ? 7 : -7;
-                } else {  // 1.5 * 2^23 rounds the exact product to an integer, ties to even
-                    q = (int)(__float_as_uint(__fmaf_rn(x[m][e], inv, 12582912.f)) - 0x4b400000u);
-                    q = q > 7 ? 7 : (q < -7 ? -7 : q);
-                }
-                word |= (uint32_t)(q + 8) << (4 * e);
+                const float q = fminf(fmaxf(__fmaf_rn(x[m][e], inv, 12582920.f), 12582913.f), 12582927.f);
+                word |= (__float_as_uint(q) & 15u) << (4 * e);
             }
             if (store) {
                 const int chunk = l + R::kLanes * m;
-                void *codes = is_v ? a.c.v_codes : a.c.k_codes, *scales = is_v ? a.c.v_scales : a.c.k_scales;
-                static_cast<uint32_t *>(codes)[row * (D / 8) + chunk] = word;
-                if ((l & 3) == 0) static_cast<__half *>(scales)[row * (D / 32) + chunk / 4] = hs;
+                codes[chunk] = word;
+                if ((l & 3) == 0) scales[chunk / 4] = hs;
             }
         }
     }
@@ -297,7 +359,7 @@ extern "C" strata_status strata_kv4_append(const strata_kv4_cache *cache, strata
     static const RopeTable none = {};
     const RopeTable &tab = rope ? rope->table : none;
     AppendArgs a{*cache, static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v),
-                 k_token_stride, v_token_stride, positions, slots, n_tokens, 1, tab.rd % 16 == 0};
+                 k_token_stride, v_token_stride, positions, slots, n_tokens, 1};
     // whole blocks of rows, but no more tokens than leave every SM a block
     const int lanes = cache->head_dim == 256 ? 8 : 4;
     int64_t tpb = kThreads / lanes / (2 * (int64_t)cache->n_kv_heads);
@@ -310,12 +372,27 @@ extern "C" strata_status strata_kv4_append(const strata_kv4_cache *cache, strata
     if (grid > 0x7fffffff) return strata_set_error(STRATA_ERR_INVALID_ARG, "n_tokens %lld", (long long)n_tokens);
     const size_t smem = (size_t)tpb * (tab.rd / 2) * sizeof(float2);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int mode = tab.rd == 0                                    ? kPlain
+                     : tab.half && tab.rd == cache->head_dim ? kHalfWhole
+                     : !tab.half && tab.rd % 8 == 0          ? kInterleaved
+                                                             : kOther;
+    auto launch = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (mode == kPlain)
+            k_kv4_append<D, kPlain><<<(int)grid, kThreads, 0, st>>>(tab, a);
+        else if (mode == kHalfWhole)
+            k_kv4_append<D, kHalfWhole><<<(int)grid, kThreads, smem, st>>>(tab, a);
+        else if (mode == kInterleaved)
+            k_kv4_append<D, kInterleaved><<<(int)grid, kThreads, smem, st>>>(tab, a);
+        else
+            k_kv4_append<D, kOther><<<(int)grid, kThreads, smem, st>>>(tab, a);
+    };
     if (cache->head_dim == 64)
-        k_kv4_append<64><<<(int)grid, kThreads, smem, st>>>(tab, a);
+        launch(std::integral_constant<int, 64>{});
     else if (cache->head_dim == 128)
-        k_kv4_append<128><<<(int)grid, kThreads, smem, st>>>(tab, a);
+        launch(std::integral_constant<int, 128>{});
     else
-        k_kv4_append<256><<<(int)grid, kThreads, smem, st>>>(tab, a);
+        launch(std::integral_constant<int, 256>{});
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return strata_set_error(STRATA_ERR_CUDA, "kv4 append launch: %s", cudaGetErrorString(e));
     return STRATA_OK;

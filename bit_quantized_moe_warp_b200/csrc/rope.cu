@@ -6,8 +6,10 @@
 // product in fp32 would be off by whole radians at far ones.
 //
 // The kernel streams every row once (2 bytes in, 2 out per value) and is bound
-// by HBM. A block takes a token at a time: its cosines and sines are computed
-// once (fp64, rotary_dim / 2 of them) into shared memory and serve every head.
+// by HBM. A block takes a few tokens at a time: their cosines and sines are
+// computed once (fp64, rotary_dim / 2 a token, one for each thread) into shared
+// memory and serve every head; a thread's first chunk is on its way meanwhile,
+// and later on the next one while a chunk is turned.
 #include <cmath>
 #include <new>
 
@@ -27,54 +29,85 @@ struct RopeArgs {
     int64_t x_tok, x_head, o_tok, o_head;
     int64_t n_tokens;
     int heads, D;
+    int tokens_per_block, items;  // items: of a head
+    uint64_t heads_inv, items_inv;  // for quotient()
 };
+
+// x / d for 0 <= x < 2^31 as a product with inv = 2^64 / d, rounded up (0 for
+// d = 1): exact, since the rounding adds less than 2^-33 to the quotient
+uint64_t inverse(int d) { return d > 1 ? ~0ull / (uint64_t)d + 1 : 0; }
+__device__ __forceinline__ int quotient(int x, uint64_t inv) { return inv ? (int)__umul64hi((uint64_t)(uint32_t)x, inv) : x; }
 
 // Whole 16-byte chunks: for the half layout a chunk of first halves and its
 // chunk of second halves, for the interleaved one four pairs in one chunk;
 // chunks past rotary_dim are copied. Every item reads and writes only its own
 // values, so out may be x.
-__global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ RopeTable tab, RopeArgs a) {
-    __shared__ float2 cs[STRATA_ROPE_MAX_HEAD_DIM / 2];
+template <bool HALF>
+__global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a) {
+    __shared__ __align__(16) float2 cs[kThreads];  // [token][pair]
     const int pairs = tab.rd / 2;
-    const int rot = tab.half ? tab.rd / 16 : tab.rd / 8;   // rotated items of a head
-    const int items = rot + (a.D - tab.rd) / 8;
-    for (int64_t t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
-        const int pos = a.positions[t];
-        for (int i = threadIdx.x; i < pairs; i += kThreads) cs[i] = rope_cs(tab, i, pos);
+    const int rot = HALF ? tab.rd / 16 : tab.rd / 8;  // rotated items of a head
+    struct Item {
+        uint4 u, v;
+        __nv_bfloat16 *out;
+        int c, t;
+    };
+    for (int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block; t0 < a.n_tokens; t0 += (int64_t)gridDim.x * a.tokens_per_block) {
+        const int nt = (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0);
+        const int total = nt * a.heads * a.items;
+        auto fetch = [&](Item &x, int it) {
+            const int th = quotient(it, a.items_inv);
+            x.c = it - th * a.items;
+            x.t = quotient(th, a.heads_inv);
+            const int h = th - x.t * a.heads;
+            const int64_t t = t0 + x.t;
+            const int e = x.c < rot ? x.c * 8 : tab.rd + (x.c - rot) * 8;
+            const __nv_bfloat16 *xr = a.x + t * a.x_tok + h * a.x_head + e;
+            x.out = a.out + t * a.o_tok + h * a.o_head + e;
+            x.u = *reinterpret_cast<const uint4 *>(xr);
+            if (HALF && x.c < rot) x.v = *reinterpret_cast<const uint4 *>(xr + pairs);
+        };
+        Item cur, next;
+        int it = threadIdx.x;
+        if (it < total) fetch(next, it);
+        const int lt = threadIdx.x / pairs;
+        if (lt < nt) cs[threadIdx.x] = rope_cs(tab, threadIdx.x - lt * pairs, a.positions[t0 + lt]);
         __syncthreads();
-        for (int it = threadIdx.x; it < items * a.heads; it += kThreads) {
-            const int h = it / items, c = it - h * items;
-            const __nv_bfloat16 *xr = a.x + t * a.x_tok + h * a.x_head;
-            __nv_bfloat16 *orow = a.out + t * a.o_tok + h * a.o_head;
-            if (c >= rot) {  // not rotated
-                const int e = tab.rd + (c - rot) * 8;
-                *reinterpret_cast<uint4 *>(orow + e) = *reinterpret_cast<const uint4 *>(xr + e);
-            } else if (tab.half) {
-                const uint4 u4 = *reinterpret_cast<const uint4 *>(xr + c * 8);
-                const uint4 v4 = *reinterpret_cast<const uint4 *>(xr + pairs + c * 8);
-                const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+        for (; it < total; it += kThreads) {
+            cur = next;
+            if (it + kThreads < total) fetch(next, it + kThreads);
+            if (cur.c >= rot) {  // not rotated
+                *reinterpret_cast<uint4 *>(cur.out) = cur.u;
+                continue;
+            }
+            // four or eight pairs, two for each 16-byte load
+            const float4 *c = reinterpret_cast<const float4 *>(cs + cur.t * pairs + cur.c * (HALF ? 8 : 4));
+            const uint32_t u[4] = {cur.u.x, cur.u.y, cur.u.z, cur.u.w};
+            if constexpr (HALF) {
+                const uint32_t v[4] = {cur.v.x, cur.v.y, cur.v.z, cur.v.w};
                 uint32_t ru[4], rv[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 c0 = cs[c * 8 + 2 * j], c1 = cs[c * 8 + 2 * j + 1];
+                    const float4 k = c[j];
+                    const float2 c0 = make_float2(k.x, k.y), c1 = make_float2(k.z, k.w);
                     ru[j] = pack_bf16(rope_first(bf16_lo(u[j]), bf16_lo(v[j]), c0),
                                       rope_first(bf16_hi(u[j]), bf16_hi(v[j]), c1));
                     rv[j] = pack_bf16(rope_second(bf16_lo(u[j]), bf16_lo(v[j]), c0),
                                       rope_second(bf16_hi(u[j]), bf16_hi(v[j]), c1));
                 }
-                *reinterpret_cast<uint4 *>(orow + c * 8) = make_uint4(ru[0], ru[1], ru[2], ru[3]);
-                *reinterpret_cast<uint4 *>(orow + pairs + c * 8) = make_uint4(rv[0], rv[1], rv[2], rv[3]);
+                *reinterpret_cast<uint4 *>(cur.out) = make_uint4(ru[0], ru[1], ru[2], ru[3]);
+                *reinterpret_cast<uint4 *>(cur.out + pairs) = make_uint4(rv[0], rv[1], rv[2], rv[3]);
             } else {
-                const uint4 w4 = *reinterpret_cast<const uint4 *>(xr + c * 8);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
                 uint32_t r[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 c0 = cs[c * 4 + j];
-                    r[j] = pack_bf16(rope_first(bf16_lo(w[j]), bf16_hi(w[j]), c0),
-                                     rope_second(bf16_lo(w[j]), bf16_hi(w[j]), c0));
+                for (int j = 0; j < 4; j += 2) {
+                    const float4 k = c[j / 2];
+                    const float2 c0 = make_float2(k.x, k.y), c1 = make_float2(k.z, k.w);
+                    r[j] = pack_bf16(rope_first(bf16_lo(u[j]), bf16_hi(u[j]), c0), rope_second(bf16_lo(u[j]), bf16_hi(u[j]), c0));
+                    r[j + 1] = pack_bf16(rope_first(bf16_lo(u[j + 1]), bf16_hi(u[j + 1]), c1),
+                                         rope_second(bf16_lo(u[j + 1]), bf16_hi(u[j + 1]), c1));
                 }
-                *reinterpret_cast<uint4 *>(orow + c * 8) = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4 *>(cur.out) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
         __syncthreads();  // cs is written again
@@ -200,13 +233,28 @@ extern "C" strata_status strata_rope_apply(strata_rope rope, const void *x, int6
         return strata_set_error(STRATA_ERR_INVALID_ARG, "token strides must hold the heads of a token");
     if (n_heads > (1 << 20)) return strata_set_error(STRATA_ERR_INVALID_ARG, "n_heads %d", n_heads);
     RopeArgs a{static_cast<const __nv_bfloat16 *>(x), static_cast<__nv_bfloat16 *>(out), positions,
-               x_token_stride, x_head_stride, out_token_stride, out_head_stride, n_tokens, n_heads, D};
+               x_token_stride, x_head_stride, out_token_stride, out_head_stride, n_tokens, n_heads, D, 1, 0, 0, 0};
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = (int)(n_tokens < 65536 ? n_tokens : 65536);
-    if (rope->table.rd % (rope->table.half ? 16 : 8) == 0)
-        k_rope_vec<<<grid, kThreads, 0, st>>>(rope->table, a);
-    else
-        k_rope_scalar<<<grid, kThreads, 0, st>>>(rope->table, a);
+    const RopeTable &tab = rope->table;
+    if (tab.rd % (tab.half ? 16 : 8) == 0) {
+        // as many tokens as threads have pairs to compute, but four blocks for every SM first
+        a.items = (tab.half ? tab.rd / 16 : tab.rd / 8) + (D - tab.rd) / 8;
+        const int64_t fit = ((int64_t)1 << 26) / ((int64_t)n_heads * a.items);  // 32-bit indices
+        int64_t most = kThreads / (tab.rd / 2);
+        most = most < fit ? most : fit;
+        const int64_t spread = (n_tokens + 4 * 148 - 1) / (4 * 148);
+        a.tokens_per_block = (int)(most < spread ? most : spread);
+        a.heads_inv = inverse(n_heads);
+        a.items_inv = inverse(a.items);
+        const int64_t blocks = (n_tokens + a.tokens_per_block - 1) / a.tokens_per_block;
+        const int grid = (int)(blocks < 65536 ? blocks : 65536);
+        if (tab.half)
+            k_rope_vec<true><<<grid, kThreads, 0, st>>>(tab, a);
+        else
+            k_rope_vec<false><<<grid, kThreads, 0, st>>>(tab, a);
+    } else {
+        k_rope_scalar<<<(int)(n_tokens < 65536 ? n_tokens : 65536), kThreads, 0, st>>>(tab, a);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return strata_set_error(STRATA_ERR_CUDA, "rotary launch: %s", cudaGetErrorString(e));
     return STRATA_OK;
