@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
     __shared__ int64_t s_before;
     __shared__ int s_b;
     griddep_launch_dependents();
+    griddep_wait();
 
     // ---- this CTA's run of units, and the sequence it starts in
     int64_t total = 0, u_lo = 0, u_hi = 0, run = 0, inc = 0, v = 0;
@@ -193,29 +194,69 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
         }
         __syncthreads();
     };
-    for (int b0 = 0; b0 < a.d.n_seqs; b0 += kChunk) scan(b0);
+    // Up to 64 sequences: every warp for itself, two for each lane
+    const bool few = a.d.n_seqs <= 64;
+    Seq mine[2] = {};
+    if (few) {
+        int64_t w[2], upto = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            w[k] = 0;
+            if (2 * lane + k < a.d.n_seqs) {
+                mine[k] = seq_of(a, 2 * lane + k, ROWS);
+                w[k] = (int64_t)seq_units(mine[k]) * mine[k].groups * a.c.n_kv_heads;
+            }
+        }
+        upto = w[0] + w[1];
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(kFullMask, upto, x);
+            if (lane >= x) upto += o;
+        }
+        run = __shfl_sync(kFullMask, upto, 31);
+        inc = upto, v = w[0] + w[1];
+    } else {
+        for (int b0 = 0; b0 < a.d.n_seqs; b0 += kChunk) scan(b0);
+    }
     total = run;
     ctas = (int)min(total, (int64_t)C::CTAS);  // a unit each at least
+    Seq s{};
+    int b = 0;
+    int64_t before = 0;
     if (blockIdx.x < ctas) {
         u_lo = run_start(total, blockIdx.x, ctas);
         u_hi = run_start(total, blockIdx.x + 1, ctas);
-        int b0 = 0;
-        if (a.d.n_seqs > kChunk) {
-            run = 0;
-            for (b0 = -kChunk; run <= u_lo;) scan(b0 += kChunk);
+        if (few) {
+            const int src = __ffs(__ballot_sync(kFullMask, u_lo < inc)) - 1;
+            const int64_t w0 = (int64_t)seq_units(mine[0]) * mine[0].groups * a.c.n_kv_heads;
+            const bool second = 2 * lane + 1 < a.d.n_seqs && inc - v + w0 <= u_lo;
+            const Seq t = second ? mine[1] : mine[0];
+            b = 2 * src + (__shfl_sync(kFullMask, second ? 1 : 0, src));
+            before = __shfl_sync(kFullMask, second ? inc - v + w0 : inc - v, src);
+            s.t0 = __shfl_sync(kFullMask, t.t0, src);
+            s.n = __shfl_sync(kFullMask, t.n, src), s.L = __shfl_sync(kFullMask, t.L, src);
+            s.tile0 = __shfl_sync(kFullMask, t.tile0, src), s.tiles = __shfl_sync(kFullMask, t.tiles, src);
+            s.groups = __shfl_sync(kFullMask, t.groups, src);
+        } else {
+            int b0 = 0;
+            if (a.d.n_seqs > kChunk) {
+                run = 0;
+                for (b0 = -kChunk; run <= u_lo;) scan(b0 += kChunk);
+            }
+            if (inc - v <= u_lo && u_lo < inc) {
+                s_b = b0 + threadIdx.x;
+                s_before = inc - v;
+            }
+            __syncthreads();
+            b = uniform(s_b);
+            before = s_before;
+            s = seq_of(a, b, ROWS);
         }
-        if (inc - v <= u_lo && u_lo < inc) {
-            s_b = b0 + threadIdx.x;
-            s_before = inc - v;
-        }
-        __syncthreads();
     }
     Span *spans = static_cast<Span *>(a.workspace);
     float *parts = reinterpret_cast<float *>(spans + kSplitMaxCtas);
     if (threadIdx.x == 0) spans[blockIdx.x].parts = 0;
     if (u_lo == u_hi) return;
-    int b = uniform(s_b);
-    Seq s = seq_of(a, b, ROWS);
     auto settle = [&]() {
         s.n = uniform(s.n), s.L = uniform(s.L), s.tile0 = uniform(s.tile0), s.tiles = uniform(s.tiles);
         s.groups = uniform(s.groups);
@@ -223,8 +264,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
     settle();
     // from here on units count from u_lo
     int per = seq_units(s);
-    int vh = uniform((int)run_start(u_lo - s_before, 1, per));  // (KV head, row group) inside the sequence
-    int first = uniform((int)(s_before + (int64_t)vh * per - u_lo));  // its first unit
+    int vh = uniform((int)run_start(u_lo - before, 1, per));  // (KV head, row group) inside the sequence
+    int first = uniform((int)(before + (int64_t)vh * per - u_lo));  // its first unit
     const int units = uniform((int)(u_hi - u_lo));
     const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)0x80000000);
     const uint32_t ring_u = smem_u32(ring), scratch_u = smem_u32(scratch);
@@ -641,8 +682,8 @@ cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t s
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_attn_split<D, NT>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    k_attn_split<D, NT><<<C::CTAS, kSplitWarps * 32, C::SMEM, st>>>(tab, a);
-    return launch_join<D, C::ROWS, 8>(a, C::CTAS, st);
+    const cudaError_t l = launch_early(k_attn_split<D, NT>, dim3(C::CTAS), kSplitWarps * 32, C::SMEM, st, tab, a);
+    return l != cudaSuccess ? l : launch_join<D, C::ROWS, 8>(a, C::CTAS, st);
 }
 
 }  // namespace

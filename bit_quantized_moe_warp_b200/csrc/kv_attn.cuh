@@ -86,13 +86,16 @@ struct Span {  // what k_attn_join needs of the last piece of a CTA
 };
 
 // One block for each piece that several CTAs share and 16 / WPR of its query
-// rows at a time: WPR warps over the parts of a row, then over each other, in a
-// fixed order. Few rows of many parts take 8 warps, many rows of few parts 1.
+// rows at a time: WPR warps over the parts of a row, each with a running
+// maximum of its own, then over each other, in a fixed order. Few rows of many
+// parts take 8 warps, many rows of few parts 1. Bound by the latency of its two
+// dependent loads, the span and the parts.
 template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
-    constexpr int P = D / 32, PART = D + 4;
+    constexpr int P = D / 32, PART = D + 4, BATCH = P == 8 ? 2 : 4;
     constexpr int RPB = 16 / WPR;
-    __shared__ float so[WPR][RPB][D], sl[WPR][RPB], sw[RPB][kSplitMaxCtas];
+    __shared__ float so[WPR][RPB][D], sl[WPR][RPB], sm[WPR][RPB];
+    griddep_launch_dependents();
     griddep_wait();
     const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
     if (sp.parts == 0) return;
@@ -102,54 +105,85 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
     for (int r0 = RPB * blockIdx.y; r0 < sp.rows; r0 += RPB * gridDim.y) {
         const int r = r0 + wr;
         const bool live = r < sp.rows;
-        auto at = [&](int i) {
-            return parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
-        };
-        float m = -FLT_MAX;
-        if (live)
-            for (int i = lane; i < sp.parts; i += 32) m = fmaxf(m, at(i)[D]);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-        float v[P], sum = 0.f;
+        float v[P], sum = 0.f, m = -FLT_MAX;
 #pragma unroll
         for (int j = 0; j < P; ++j) v[j] = 0.f;
-        if (live) {
-            for (int i = wq + WPR * lane; i < sp.parts; i += 32 * WPR) {  // the parts of this warp
-                const float f = ex2(at(i)[D] - m);
-                sw[wr][i] = f;
-                sum = fmaf(at(i)[D + 1], f, sum);
-            }
-            __syncwarp();
-#pragma unroll 4
-            for (int i = wq; i < sp.parts; i += WPR) {
-                const float f = sw[wr][i];
-                float w[P];
-                if constexpr (P == 2) *reinterpret_cast<float2 *>(w) = *reinterpret_cast<const float2 *>(at(i) + lane * P);
+        for (int i0 = wq; i0 < sp.parts && live; i0 += WPR * BATCH) {
+            float w[BATCH][P];
+            float2 ml[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = i0 + WPR * k;
+                ml[k] = make_float2(-FLT_MAX, 0.f);
+#pragma unroll
+                for (int j = 0; j < P; ++j) w[k][j] = 0.f;
+                if (i >= sp.parts) continue;
+                const float *p = parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
+                ml[k] = *reinterpret_cast<const float2 *>(p + D);
+                if constexpr (P == 2) *reinterpret_cast<float2 *>(w[k]) = *reinterpret_cast<const float2 *>(p + lane * P);
                 if constexpr (P >= 4)
 #pragma unroll
                     for (int j = 0; j < P; j += 4)
-                        *reinterpret_cast<float4 *>(w + j) = *reinterpret_cast<const float4 *>(at(i) + lane * P + j);
+                        *reinterpret_cast<float4 *>(w[k] + j) = *reinterpret_cast<const float4 *>(p + lane * P + j);
+            }
+            float top = m;
 #pragma unroll
-                for (int j = 0; j < P; ++j) v[j] = fmaf(w[j], f, v[j]);
+            for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+            const float f = ex2(m - top);
+            m = top;
+            sum *= f;
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] *= f;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const float g = ex2(ml[k].x - m);
+                sum = fmaf(ml[k].y, g, sum);
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[j] = fmaf(w[k][j], g, v[j]);
             }
         }
+        if constexpr (WPR > 1) {
 #pragma unroll
-        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFullMask, sum, x);
+            for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
+            if (lane == 0) sl[wq][wr] = sum, sm[wq][wr] = m;
+            __syncthreads();
+            if (wq == 0) {
+                float top = m;
 #pragma unroll
-        for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
-        if (lane == 0) sl[wq][wr] = sum;
-        __syncthreads();
-        if (wq == 0 && live) {
+                for (int w = 1; w < WPR; ++w) top = fmaxf(top, sm[w][wr]);
+                const float f = ex2(m - top);
+                sum *= f;
 #pragma unroll
-            for (int w = 1; w < WPR; ++w) {
-                sum += sl[w][wr];
+                for (int j = 0; j < P; ++j) v[j] *= f;
 #pragma unroll
-                for (int j = 0; j < P; ++j) v[j] += so[w][wr][lane * P + j];
+                for (int w = 1; w < WPR; ++w) {
+                    const float g = ex2(sm[w][wr] - top);
+                    sum = fmaf(sl[w][wr], g, sum);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) v[j] = fmaf(so[w][wr][lane * P + j], g, v[j]);
+                }
             }
-            store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
         }
-        __syncthreads();
+        if (wq == 0 && live) store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
+        if constexpr (WPR > 1) __syncthreads();
     }
+}
+
+// A launch that may come up before the kernel in front of it in the stream has
+// ended: the kernels wait (griddep_wait) before they touch memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Args &...args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Dynamic shared memory of a kernel, set once for each device: done has a bit each
@@ -167,19 +201,10 @@ cudaError_t allow_smem(Kernel *kernel, int bytes, std::atomic<uint64_t> &done) {
 
 template <int D, int ROWS, int WPR>
 cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
-    // programmatic launch: the blocks come up while the last CTAs finish
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     const int64_t rows = (int64_t)a.d.max_q_len * a.group;  // a hint only: a block takes more rows in turn
     constexpr int RPB = 16 / WPR;
-    cfg.gridDim = dim3(ctas, rows < 1 ? 1 : rows < ROWS ? (unsigned)(rows + RPB - 1) / RPB : ROWS / RPB);
-    cfg.blockDim = dim3(512);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<D, ROWS, WPR>, a);
+    const unsigned y = rows < 1 ? 1 : rows < ROWS ? (unsigned)(rows + RPB - 1) / RPB : ROWS / RPB;
+    return launch_early(k_attn_join<D, ROWS, WPR>, dim3(ctas, y), 512, 0, st, a);
 }
 
 // Many query rows (kv_attn_tiles.cu): bytes of its partial results, and the launch

@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
 
+    griddep_wait();
+
     // ---- this CTA's run of units, and the item that it starts in
     int64_t run = 0, inc = 0, v = 0;
     auto scan = [&](int b0) {  // inc: units up to and with sequence b0 + threadIdx.x; run: with the whole chunk
@@ -915,8 +917,8 @@ cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_attn_tiles<D>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    k_attn_tiles<D><<<kSms, kThreads, C::SMEM, st>>>(tab, a);
-    return launch_join<D, C::ROWS, 1>(a, kSms, st);
+    const cudaError_t l = launch_early(k_attn_tiles<D>, dim3(kSms), kThreads, C::SMEM, st, tab, a);
+    return l != cudaSuccess ? l : launch_join<D, C::ROWS, 1>(a, kSms, st);
 }
 
 }  // namespace
