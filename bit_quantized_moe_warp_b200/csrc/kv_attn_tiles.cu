@@ -115,6 +115,18 @@ STRATA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" :
 STRATA_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(kFullMask, mbar_wait(bar, parity, nullptr, abort));
 }
+// by a whole warp: until a number in shared memory has come up to `least`
+STRATA_DEV bool count_wait(volatile uint32_t *count, uint32_t least, volatile int *abort) {
+    const uint64_t t0 = globaltimer();
+    bool ok = true;
+    for (uint32_t i = 1; ok && *count < least; ++i)
+        if ((i & 63u) == 0 && (*abort || globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            ok = false;
+        }
+    __threadfence_block();
+    return __all_sync(kFullMask, ok);
+}
 // barrier of `threads` threads; whether any of them says stop
 STRATA_DEV bool named_barrier_or(int id, int threads, bool stop) {
     uint32_t any;
@@ -233,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint64_t kfull[2], vfull[2], kempty[2], vempty[2], sfull[2], pready[2], pvdone, odone, qfull;
     __shared__ uint32_t tmem_base;
     __shared__ int s_abort, s_b;
+    __shared__ uint32_t s_begun;  // pieces whose rows are there: the results of those before are out
     __shared__ int64_t s_sum[kThreads / 32], s_before;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     griddep_launch_dependents();
@@ -254,22 +267,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&odone, 1);
         mbar_init(&qfull, 8);
         s_abort = 0;
+        s_begun = 0;
         fence_mbar_init();
     }
 
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
     griddep_wait();
 
     // ---- this CTA's run of units, and the item that it starts in
     int64_t run = 0, inc = 0, v = 0;
-    auto scan = [&](int b0) {  // inc: units up to and with sequence b0 + threadIdx.x; run: with the whole chunk
-        const int b = b0 + threadIdx.x;
+    // the units of 32 sequences, by a whole warp; inc: up to and with b0 + lane
+    auto scan32 = [&](int b0, SeqBase &s) {
+        const int b = b0 + lane;
         v = 0;
-        SeqBase s{0, 0, 0};
+        s = SeqBase{0, 0, 0};
         if (b < a.d.n_seqs) load_seq(s, a, b);
         const int count = item_count(a, s.n, C::ROWS);
         for (int rt = 0; rt < count && count <= 4; ++rt) v += item_units(item_of<D>(a, s, rt));
         for (uint32_t many = __ballot_sync(kFullMask, count > 4); many; many &= many - 1) {
-            const int src = __ffs(many) - 1;  // long prompts: the whole warp
+            const int src = __ffs(many) - 1;  // long prompts: the lanes together
             const SeqBase o{0, __shfl_sync(kFullMask, s.n, src), __shfl_sync(kFullMask, s.L, src)};
             const int64_t sum = head_units<D>(a, o, lane);
             if (lane == src) v = sum;
@@ -281,6 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t o = __shfl_up_sync(kFullMask, inc, x);
             if (lane >= x) inc += o;
         }
+    };
+    auto scan = [&](int b0) {  // the same by the block; run: with the whole chunk
+        SeqBase s;
+        scan32(b0 + warp * 32, s);
         if (lane == 31) s_sum[warp] = inc;
         __syncthreads();
         inc += run;
@@ -291,15 +314,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
     };
-    for (int b0 = 0; b0 < a.d.n_seqs; b0 += kThreads) scan(b0);
+    // Up to 32 sequences: every warp for itself
+    const bool few = a.d.n_seqs <= 32;
+    SeqBase s{0, 0, 0};
+    if (few) {
+        scan32(0, s);
+        run = __shfl_sync(kFullMask, inc, 31);
+    } else {
+        for (int b0 = 0; b0 < a.d.n_seqs; b0 += kThreads) scan(b0);
+    }
     const int64_t total = run;
     const int ctas = (int)min(total, (int64_t)kSms);  // a unit each at least
     Span *spans = static_cast<Span *>(a.workspace);
     float *parts = reinterpret_cast<float *>(spans + kSplitMaxCtas);
     if (threadIdx.x == 0) spans[blockIdx.x].parts = 0;
-    if (blockIdx.x >= ctas) return;
-    const int64_t u_lo = run_start(total, blockIdx.x, ctas), u_hi = run_start(total, blockIdx.x + 1, ctas);
-    {
+    const bool idle = blockIdx.x >= ctas;
+    const int64_t u_lo = idle ? 0 : run_start(total, blockIdx.x, ctas), u_hi = idle ? 0 : run_start(total, blockIdx.x + 1, ctas);
+    if (!few && !idle) {
         int b0 = 0;
         if (a.d.n_seqs > kThreads) {
             run = 0;
@@ -310,23 +341,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_before = inc - v;
         }
     }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&tmem_base, 512);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = tmem_base;
+    if (idle) {
+        if (warp == kMmaWarp) tmem_dealloc(tbase, 512);
+        return;
+    }
 
-    int b = uniform(s_b), hk = 0, rt = 0, first;  // units count from u_lo; first: of the item
-    SeqBase s;
-    load_seq(s, a, b);
+    int b, hk = 0, rt = 0, first;  // units count from u_lo; first: of the item
+    int64_t before;
+    if (few) {
+        b = __ffs(__ballot_sync(kFullMask, u_lo < inc)) - 1;
+        before = __shfl_sync(kFullMask, inc - v, b);
+        s = SeqBase{__shfl_sync(kFullMask, s.t0, b), __shfl_sync(kFullMask, s.n, b), __shfl_sync(kFullMask, s.L, b)};
+    } else {
+        b = uniform(s_b);
+        before = s_before;
+        load_seq(s, a, b);
+    }
     Item it;
     {
         const int64_t per = head_units<D>(a, s, lane);
-        hk = uniform((int)run_start(u_lo - s_before, 1, per));
-        int64_t rem = u_lo - s_before - hk * per;
+        hk = uniform((int)run_start(u_lo - before, 1, per));
+        int64_t rem = u_lo - before - hk * per;
         for (;; rt += 32) {  // the item that holds unit `rem`
             const int n = rt + lane < item_count(a, s.n, C::ROWS) ? item_units(item_of<D>(a, s, rt + lane)) : 0;
             int64_t upto = n;
@@ -480,8 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             find(0);
             load(0);
             find(1);
-            // the second O of the last piece was added up in the keys' buffers
-            if (p.nt > 0 && p.after_dual && !warp_wait(&qfull, p.count & 1, &s_abort)) return false;
+            // The second O of the last dual piece was added up in the keys' buffers. These
+            // warps may be pieces ahead, where a barrier's parity says nothing: a count.
+            if (p.nt > 0 && p.after_dual && !count_wait(&s_begun, p.count + 1, &s_abort)) return false;
             for (int jj = 0; jj < p.nt; ++jj) {
                 const uint32_t c = p.tc + jj;
                 // the scales' ranges decide for 32 keys at a time; keys and values see the same numbers
@@ -569,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             {
                 using Q = QueryRow<D>;
                 const int shift = p.dual && p.it.rows <= 64 ? 64 : 0;
-                constexpr int BATCH = 2;
+                constexpr int BATCH = D == 64 ? 8 : D == 128 ? 4 : 2;
                 const int run = (min(p.it.rows, p.dual || SLOTS == 1 ? 128 : 256) + 7) / 8;  // 32 at most
                 const int end = min(warp * run + run, p.it.rows);
                 auto tok_of = [&](int r) { return p.s.t0 + by_group(a, p.it.row0 + min(max(r, 0), p.it.rows - 1)); };
@@ -639,6 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 // the factors are read by other warps; a wait that ran out ends the work for all of them
                 if (named_barrier_or(2, 256, *(volatile int *)&s_abort != 0)) return false;
+                if (threadIdx.x == 0) {
+                    __threadfence_block();
+                    *(volatile uint32_t *)&s_begun = p.count + 1;
+                }
                 if (lane == 0) mbar_arrive(&qfull);
             }
             const int slot = warp >> 2, tr = threadIdx.x & 127;
@@ -839,38 +883,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float norm = p.whole ? bad * (l > 0.f ? rsqrt_dim<D>() / l : 0.f) : bad;
                 f0 *= norm, f1 *= norm;
                 if ((!p.dual || slot == 0) && busy) {
-                    auto row16 = [&](float (&x)[16], int col) {  // 16 columns, values in order
-                        float y[16];
-                        tmem_ld16(ocol + col, y);
+                    auto row32 = [&](float (&x)[32], int col) {  // 32 columns, values in order
+                        float y[32];
+                        tmem_ld32(ocol + col, y);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
+                        for (int e = 0; e < 32; ++e) {
                             float z = mine ? y[e] * f0 : 0.f;
                             if (p.dual && p.nt > 1) z = fmaf(other[(col + e) * 128 + r], f1, z);
-                            x[(e & 8) + value_at(e & 7)] = z;
+                            x[(e & 24) + value_at(e & 7)] = z;
                         }
                     };
                     if (p.whole) {
                         const int i = by_group(a, p.it.row0 + r), h = p.hk * a.group + p.it.row0 + r - i * a.group;
                         __nv_bfloat16 *dst = a.out + (p.s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
-                        // H of D = H of D / 16 over H of 16: 16 values of the result at a time
+                        // H of D = H of D / 32 over H of 32: 32 values of the result at a time
 #pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
-                            float x[16];
+                        for (int q = 0; q < D / 32; ++q) {
+                            float x[32];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] = 0.f;
-#pragma unroll 2
-                            for (int j = 0; j < D / 16; ++j) {
+                            for (int e = 0; e < 32; ++e) x[e] = 0.f;
+#pragma unroll 1
+                            for (int j = 0; j < D / 32; ++j) {
                                 const float sg = __popc(j & q) & 1 ? -1.f : 1.f;
-                                float y[16];
-                                row16(y, 16 * j);
+                                float y[32];
+                                row32(y, 32 * j);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) x[e] = fmaf(sg, y[e], x[e]);
+                                for (int e = 0; e < 32; ++e) x[e] = fmaf(sg, y[e], x[e]);
                             }
 #pragma unroll
-                            for (int d = 1; d < 16; d <<= 1)
+                            for (int d = 1; d < 32; d <<= 1)
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
+                                for (int e = 0; e < 32; ++e)
                                     if (!(e & d)) {
                                         const float y = x[e], z = x[e + d];
                                         x[e] = y + z;
@@ -878,8 +922,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     }
                             if (store) {
 #pragma unroll
-                                for (int e = 0; e < 16; e += 8)
-                                    *reinterpret_cast<uint4 *>(dst + 16 * q + e) =
+                                for (int e = 0; e < 32; e += 8)
+                                    *reinterpret_cast<uint4 *>(dst + 32 * q + e) =
                                         make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
                                                    pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
                             }
@@ -887,13 +931,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         float *part = parts + (int64_t)((blockIdx.x * 2 + (p.u ? 1 : 0)) * C::ROWS + r) * C::PART;
 #pragma unroll 1
-                        for (int g = 0; g < D / 16; ++g) {
-                            float x[16];
-                            row16(x, 16 * g);
+                        for (int g = 0; g < D / 32; ++g) {
+                            float x[32];
+                            row32(x, 32 * g);
                             if (store)
 #pragma unroll
-                                for (int e = 0; e < 16; e += 4)
-                                    *reinterpret_cast<float4 *>(part + 16 * g + e) =
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<float4 *>(part + 32 * g + e) =
                                         make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                         }
                         if (store) part[D] = M, part[D + 1] = l;
