@@ -31,11 +31,20 @@ namespace strata {
 
 constexpr unsigned kFullMask = 0xffffffffu;
 
+// Frequency of pair i. The table is a kernel parameter; lanes ask for different
+// entries, which the constant cache serves one at a time (32 replays a warp), so
+// it is read through a pointer whose origin the compiler does not see, as memory.
+__device__ __forceinline__ uint64_t rope_freq(const RopeTable &t, int i) {
+    const uint64_t *p = t.freq;
+    asm("" : "+l"(p));
+    return p[i];
+}
+
 // position * f / (2 pi) modulo one turn: the product wraps modulo 2^64, which
 // is exactly one turn, so a far position loses no bits; as a signed fraction
 // of half turns in [-1, 1).
 __device__ __forceinline__ double half_turns(const RopeTable &t, int i, int position) {
-    return (double)(int64_t)((uint64_t)(int64_t)position * t.freq[i]) * 0x1p-63;
+    return (double)(int64_t)((uint64_t)(int64_t)position * rope_freq(t, i)) * 0x1p-63;
 }
 
 // (cos, sin) of pair i: fp64, rounded once to fp32 (the bits that
@@ -50,7 +59,7 @@ __device__ __forceinline__ float2 rope_cs(const RopeTable &t, int i, int positio
 // the turn's fraction, then the hardware's sine and cosine (off by 2^-20.9 at
 // most in [-pi, pi]; the row is rounded to fp16, 2^-11, next)
 __device__ __forceinline__ float2 rope_cs_f32(const RopeTable &t, int i, int position) {
-    const int32_t turn = (int32_t)((uint64_t)((int64_t)position * (int64_t)t.freq[i]) >> 32);
+    const int32_t turn = (int32_t)((uint64_t)((int64_t)position * (int64_t)rope_freq(t, i)) >> 32);
     const float x = (float)turn * 0x1.921fb6p-30f;  // pi 2^-31 a unit
     return make_float2(__cosf(x) * (float)t.m, __sinf(x) * (float)t.m);
 }

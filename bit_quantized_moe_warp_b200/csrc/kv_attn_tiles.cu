@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             {
                 using Q = QueryRow<D>;
                 const int shift = p.dual && p.it.rows <= 64 ? 64 : 0;
-                constexpr int BATCH = D == 64 ? 8 : D == 128 ? 4 : 2;
+                constexpr int BATCH = 2;
                 const int run = (min(p.it.rows, p.dual || SLOTS == 1 ? 128 : 256) + 7) / 8;  // 32 at most
                 const int end = min(warp * run + run, p.it.rows);
                 auto tok_of = [&](int r) { return p.s.t0 + by_group(a, p.it.row0 + min(max(r, 0), p.it.rows - 1)); };
