@@ -111,21 +111,29 @@ STRATA_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         : "memory");
 }
 STRATA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// by a whole warp, which goes on or gives up together
-STRATA_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(kFullMask, mbar_wait(bar, parity, nullptr, abort));
-}
-// by a whole warp: until a number in shared memory has come up to `least`
-STRATA_DEV bool count_wait(volatile uint32_t *count, uint32_t least, volatile int *abort) {
+// Waits of a whole warp. The lanes ask together and leave the loop together: what
+// follows (.aligned instructions, uniform registers) needs the warp in one piece,
+// which lanes that leave a loop one by one do not promise.
+template <typename Test>
+STRATA_DEV bool warp_poll(Test &&test, volatile int *abort) {
+    if (__all_sync(kFullMask, test())) return true;
     const uint64_t t0 = globaltimer();
-    bool ok = true;
-    for (uint32_t i = 1; ok && *count < least; ++i)
-        if ((i & 63u) == 0 && (*abort || globaltimer() - t0 > kWaitLimitNs)) {
-            *abort = 1;
-            ok = false;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(kFullMask, test())) return true;
+        if ((i & 63u) == 0 && __any_sync(kFullMask, (abort && *abort) || globaltimer() - t0 > kWaitLimitNs)) {
+            if (abort) *abort = 1;
+            return false;
         }
+    }
+}
+STRATA_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return warp_poll([&]() { return mbar_try_wait(bar, parity); }, abort);
+}
+// until a number in shared memory has come up to `least`
+STRATA_DEV bool count_wait(volatile uint32_t *count, uint32_t least, volatile int *abort) {
+    const bool ok = warp_poll([&]() { return *count >= least; }, abort);
     __threadfence_block();
-    return __all_sync(kFullMask, ok);
+    return ok;
 }
 // barrier of `threads` threads; whether any of them says stop
 STRATA_DEV bool named_barrier_or(int id, int threads, bool stop) {
