@@ -579,12 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < C::NW; ++i) cs[i] = h2_bits(__hmul2(bits_h2(cs[i]), mul));
                 }
                 const __half2 off = __floats2half2_rn(-1032.f, -1032.f), off64 = __floats2half2_rn(-72.f, -72.f);
-                // a block of 32 values at a time, in one piece of code: the roles share the
-                // instruction cache
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < C::NW; ++i) {
-                    const uint32_t words[4] = {cw[0].x, cw[0].y, cw[0].z, cw[0].w};
-                    const __half2 sc2 = bits_h2(cs[0]);
+                    const uint32_t words[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
+                    const __half2 sc2 = bits_h2(cs[i]);
                     const uint32_t at = (to ^ ((i & 1) << 6)) + (part * (C::NW / 2) + (i >> 1)) * (TK * 128);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -598,8 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      "r"(o.z), "r"(o.w)
                                      : "memory");
                     }
-#pragma unroll
-                    for (int k = 0; k + 1 < C::NW; ++k) cw[k] = cw[k + 1], cs[k] = cs[k + 1];
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -619,33 +615,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int shift = p.dual && p.it.rows <= 64 ? 64 : 0;
                 constexpr int BATCH = 2;
                 const int run = (min(p.it.rows, p.dual || SLOTS == 1 ? 128 : 256) + 7) / 8;  // 32 at most
-                const int end = min(warp * run + run, p.it.rows);
-                auto tok_of = [&](int r) { return p.s.t0 + by_group(a, p.it.row0 + min(max(r, 0), p.it.rows - 1)); };
-                const int pos_lane = tab.rd ? a.positions[tok_of(warp * run + lane)] : 0;
+                const int end = min(warp * run + run, p.it.rows), first_row = warp * run;
+                // a lane for each row of the run: its place and its token's position
+                const int my_row = p.it.row0 + min(first_row + lane, p.it.rows - 1), my_tok = by_group(a, my_row);
+                const int64_t my_at = (p.s.t0 + my_tok) * a.d.q_token_stride +
+                                      (int64_t)(p.hk * a.group + my_row - my_tok * a.group) * D;
+                const int my_pos = tab.rd ? a.positions[p.s.t0 + my_tok] : 0;
+                const int chunk = (lane * P >> 3) & 7;  // of the row, in its block of 64 values
+                const uint32_t place = smem_u32(sq) + (lane * P >> 6) * (128 * 128) + place_of(lane * P & 7) * 2;
                 float2 cs[P];
-                int64_t at = -1;
+                int at = -1;
                 typename Q::Raw raw[BATCH], next[BATCH];
                 auto fetch = [&](int r0) {
 #pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        const int row = p.it.row0 + min(r0 + k, p.it.rows - 1), i = by_group(a, row);
-                        Q::load(next[k], a.q + (p.s.t0 + i) * a.d.q_token_stride + (int64_t)(p.hk * a.group + row - i * a.group) * D,
-                                tab, lane);
-                    }
+                    for (int k = 0; k < BATCH; ++k)
+                        Q::load(next[k], a.q + __shfl_sync(kFullMask, my_at, min(r0 + k - first_row, 31)), tab, lane);
                 };
-                fetch(warp * run);
+                fetch(first_row);
 #pragma unroll 1
-                for (int r0 = warp * run; r0 < end; r0 += BATCH) {
+                for (int r0 = first_row; r0 < end; r0 += BATCH) {
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) raw[k] = next[k];
                     fetch(r0 + BATCH);
                     float q[BATCH][P], m[BATCH];
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {  // past the end: the last row once more
-                        const int r = min(r0 + k, end - 1);
-                        if (tok_of(r) != at) {
-                            at = tok_of(r);
-                            Q::angles(cs, tab, __shfl_sync(kFullMask, pos_lane, r - warp * run), lane);
+                        const int r = min(r0 + k, end - 1) - first_row, tok = __shfl_sync(kFullMask, my_tok, r);
+                        if (tok != at) {
+                            at = tok;
+                            Q::angles(cs, tab, __shfl_sync(kFullMask, my_pos, r), lane);
                         }
                         Q::rotate(q[k], raw[k], cs, tab, lane);
                     }
@@ -669,14 +667,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (r >= end) break;  // what lies behind keeps older rows' values: never stored
                         const uint32_t ex = min(max(__float_as_uint(m[k]) >> 23, 1u), 252u);
                         const float mul = m[k] > 0.f ? __uint_as_float((253u - ex) << 23) : 1.f;  // largest value to [0.5, 1)
+                        const uint32_t to = place + (r >> 7) * C::Q + (r & 127) * 128 + ((chunk ^ (r & 7)) << 4);
 #pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            const int d = lane * P + i;
-                            const __half x = __float2half_rn(q[k][i] * mul);
-                            *reinterpret_cast<__half *>(sq + (r >> 7) * C::Q + sw_chunk(128, r & 127, d >> 3) +
-                                                        place_of(d & 7) * 2) = x;
-                            if (shift)
-                                *reinterpret_cast<__half *>(sq + C::Q + sw_chunk(128, r + 64, d >> 3) + place_of(d & 7) * 2) = x;
+                        for (int i = 0; i < P; ++i) {  // P <= 4: the lane's values are every second one of its chunk
+                            const uint16_t x = __half_as_ushort(__float2half_rn(q[k][i] * mul));
+                            const uint32_t off = P == 8 ? place_of(i) * 2 : 4 * i;
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + off), "h"(x) : "memory");
+                            if (shift) asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + off + C::Q + 64 * 128), "h"(x) : "memory");
                         }
                         // above zero, so that a masked score stays -inf
                         if (lane == 0)
@@ -701,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int shift = p.dual && p.it.rows <= 64 ? 64 * slot : 0;
             const int r = (SLOTS == 2 && !p.dual ? slot * 128 : 0) + tr - shift;  // of the item; outside it: no row
             const bool busy = __any_sync(kFullMask, r >= 0 && r < p.it.rows);
-            const int pos = p.s.L - p.s.n + by_group(a, p.it.row0 + min(r, p.it.rows - 1));
+            const int pos = p.s.L - p.s.n + by_group(a, p.it.row0 + min(max(r, 0), p.it.rows - 1));
             const int hi = min(pos, p.s.L - 1), lo = a.d.window > 0 ? (int)max((int64_t)pos - a.d.window, (int64_t)-1) : -1;
             const int full_hi = p.s.L - p.s.n + by_group(a, p.it.row0);
             const int full_lo =
@@ -796,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (plain && slow == 0) {
                     // the weights themselves tell, as fp16, whether M has to move first
-#pragma unroll 1
+#pragma unroll 2
                     for (int g = 0; g < TK / 32; ++g) {
                         float w[32];
                         uint32_t y[16];
