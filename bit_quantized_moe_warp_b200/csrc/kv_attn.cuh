@@ -90,7 +90,9 @@ struct Span {  // what k_attn_join needs of the last piece of a CTA
 // maximum of its own, then over each other, in a fixed order. Few rows of many
 // parts take 8 warps, many rows of few parts 1. Bound by the latency of its two
 // dependent loads, the span and the parts.
-template <int D, int ROWS, int WPR>
+// PLANES: a part's rows lie in planes of four values, [D / 4 + 1][ROWS] float4,
+// else as [ROWS][D + 4] floats; M and l follow the D values.
+template <int D, int ROWS, int WPR, bool PLANES>
 __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
     constexpr int P = D / 32, PART = D + 4, BATCH = P == 8 ? 2 : 4;
     constexpr int RPB = 16 / WPR;
@@ -118,13 +120,14 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
 #pragma unroll
                 for (int j = 0; j < P; ++j) w[k][j] = 0.f;
                 if (i >= sp.parts) continue;
-                const float *p = parts + (int64_t)(((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * ROWS + r) * PART;
-                ml[k] = *reinterpret_cast<const float2 *>(p + D);
-                if constexpr (P == 2) *reinterpret_cast<float2 *>(w[k]) = *reinterpret_cast<const float2 *>(p + lane * P);
+                const float *p = parts + (int64_t)((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * (ROWS * PART);
+                auto at = [&](int d) { return PLANES ? p + ((d >> 2) * ROWS + r) * 4 + (d & 3) : p + r * PART + d; };
+                ml[k] = *reinterpret_cast<const float2 *>(at(D));
+                if constexpr (P == 2) *reinterpret_cast<float2 *>(w[k]) = *reinterpret_cast<const float2 *>(at(lane * P));
                 if constexpr (P >= 4)
 #pragma unroll
                     for (int j = 0; j < P; j += 4)
-                        *reinterpret_cast<float4 *>(w[k] + j) = *reinterpret_cast<const float4 *>(p + lane * P + j);
+                        *reinterpret_cast<float4 *>(w[k] + j) = *reinterpret_cast<const float4 *>(at(lane * P + j));
             }
             float top = m;
 #pragma unroll
@@ -199,12 +202,12 @@ cudaError_t allow_smem(Kernel *kernel, int bytes, std::atomic<uint64_t> &done) {
     return e;
 }
 
-template <int D, int ROWS, int WPR>
+template <int D, int ROWS, int WPR, bool PLANES>
 cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
     const int64_t rows = (int64_t)a.d.max_q_len * a.group;  // a hint only: a block takes more rows in turn
     constexpr int RPB = 16 / WPR;
     const unsigned y = rows < 1 ? 1 : rows < ROWS ? (unsigned)(rows + RPB - 1) / RPB : ROWS / RPB;
-    return launch_early(k_attn_join<D, ROWS, WPR>, dim3(ctas, y), 512, 0, st, a);
+    return launch_early(k_attn_join<D, ROWS, WPR, PLANES>, dim3(ctas, y), 512, 0, st, a);
 }
 
 // Many query rows (kv_attn_tiles.cu): bytes of its partial results, and the launch

@@ -189,9 +189,8 @@ STRATA_DEV uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
 STRATA_DEV uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 STRATA_DEV __half2 bits_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 
-// Where 16-byte chunk c (8 values) of row r lies: blocks of 64 values, 128-byte swizzle
-STRATA_DEV uint32_t sw_chunk(int rows, int r, int c) { return (c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
-
+// Tiles of keys, values and query rows: blocks of 64 values, rows of 128 bytes in
+// 16-byte chunks of 8 values, chunk c of row r at c ^ (r & 7) (128-byte swizzle).
 // Inside 8 values the chunks hold 0 4 1 5 2 6 3 7: the order of a code word's nibble pairs
 __host__ __device__ constexpr int place_of(int n) { return n < 4 ? 2 * n : 2 * n - 7; }
 __host__ __device__ constexpr int value_at(int p) { return p & 1 ? 4 + (p >> 1) : p >> 1; }
@@ -612,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // takes rows in a run, which share a token's angles
             {
                 using Q = QueryRow<D>;
+                if (p.count) named_barrier(3, 256);  // the last piece's results went through the rows' place
                 const int shift = p.dual && p.it.rows <= 64 ? 64 : 0;
                 constexpr int BATCH = 2;
                 const int run = (min(p.it.rows, p.dual || SLOTS == 1 ? 128 : 256) + 7) / 8;  // 32 at most
@@ -900,8 +900,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     if (p.whole) {
-                        const int i = by_group(a, p.it.row0 + r), h = p.hk * a.group + p.it.row0 + r - i * a.group;
-                        __nv_bfloat16 *dst = a.out + (p.s.t0 + i) * a.d.out_token_stride + (int64_t)h * D;
                         // H of D = H of D / 32 over H of 32: 32 values of the result at a time
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
@@ -925,16 +923,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         x[e] = y + z;
                                         x[e + d] = y - z;
                                     }
-                            if (store) {
+                            // by way of the query rows' place (their products are done): a lane
+                            // has a row, and the stores want rows in one piece
 #pragma unroll
-                                for (int e = 0; e < 32; e += 8)
-                                    *reinterpret_cast<uint4 *>(dst + 32 * q + e) =
-                                        make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
-                                                   pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
-                            }
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4 *>(sq + r * (D * 2) + (((q * 4 + e / 8) ^ (r & 7)) << 4)) =
+                                    make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
+                                               pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
+                        }
+                        __syncwarp();
+                        constexpr int CH = D / 8;  // 16-byte chunks of a row
+                        const int base = r - lane, c = lane % CH;
+#pragma unroll 1
+                        for (int k = lane / CH; k < 32 && base + k < p.it.rows; k += 32 / CH) {
+                            const int row = base + k, i = by_group(a, p.it.row0 + row);
+                            const int h = p.hk * a.group + p.it.row0 + row - i * a.group;
+                            *reinterpret_cast<uint4 *>(a.out + (p.s.t0 + i) * a.d.out_token_stride + (int64_t)h * D + c * 8) =
+                                *reinterpret_cast<const uint4 *>(sq + row * (D * 2) + ((c ^ (row & 7)) << 4));
                         }
                     } else {
-                        float *part = parts + (int64_t)((blockIdx.x * 2 + (p.u ? 1 : 0)) * C::ROWS + r) * C::PART;
+                        // planes of four values over the rows: the lanes' stores lie together
+                        float4 *part = reinterpret_cast<float4 *>(parts + (int64_t)(blockIdx.x * 2 + (p.u ? 1 : 0)) * C::ROWS * C::PART) + r;
 #pragma unroll 1
                         for (int g = 0; g < D / 32; ++g) {
                             float x[32];
@@ -942,10 +951,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (store)
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4)
-                                    *reinterpret_cast<float4 *>(part + 32 * g + e) =
-                                        make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                                    part[(8 * g + e / 4) * C::ROWS] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                         }
-                        if (store) part[D] = M, part[D + 1] = l;
+                        if (store) part[(D / 4) * C::ROWS] = make_float4(M, l, 0.f, 0.f);
                     }
                 }
             }
@@ -967,7 +975,7 @@ cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     const cudaError_t e = allow_smem(k_attn_tiles<D>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     const cudaError_t l = launch_early(k_attn_tiles<D>, dim3(kSms), kThreads, C::SMEM, st, tab, a);
-    return l != cudaSuccess ? l : launch_join<D, C::ROWS, 1>(a, kSms, st);
+    return l != cudaSuccess ? l : launch_join<D, C::ROWS, 1, true>(a, kSms, st);
 }
 
 }  // namespace
