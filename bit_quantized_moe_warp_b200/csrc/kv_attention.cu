@@ -43,6 +43,12 @@ namespace {
 // most for a CTA, and k_attn_join adds them up in a fixed order.
 constexpr int kSplitParts = 2 * 16 * kSms;  // rows of partial results: 2 x 8 rows x 296 CTAs or 2 x 16 x 148
 constexpr int kSplitWarps = 8;
+// Rows of a KV head and sequence up to which k_attn_split is launched, 16 at a
+// time, and above which k_attn_tiles. us with one and the other, 8 sequences up
+// to 32,768 / 4 up to 2,000 / 1 of 100,000 keys, 4 KV heads of 128: 32 rows 52,
+// 19, 51 and 67, 25, 72; 48 rows 59, 20, 70 and 65, 28, 75; 64 rows 133, 20, 87
+// and 157, 28, 76. Both take any number.
+constexpr int kSplitMostRows = 48;
 constexpr int kStages = 2;  // a warp's own work on a tile covers the latency of the next
 constexpr int kTile = 32;   // keys, as two halves of 16: no half crosses a page
 
@@ -740,7 +746,7 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool two = (int64_t)d->max_q_len * a.group > 8;
     cudaError_t e;
-    if ((int64_t)d->max_q_len * a.group > 16)
+    if ((int64_t)d->max_q_len * a.group > kSplitMostRows)
         e = launch_attn_tiles(tab, a, st);
     else if (cache->head_dim == 64)
         e = two ? launch_split<64, 2>(tab, a, st) : launch_split<64, 1>(tab, a, st);

@@ -110,6 +110,30 @@ def test_append_bits(D, heads, page, n):
         assert np.array_equal(t.view(torch.uint8).cpu().numpy(), w)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("share,layout", [(1.0, "half"), (0.5, "half"), (0.25, "half"), (1.0, "interleaved"), (0.25, "interleaved"),
+                                          (0.0, "half")])
+@pytest.mark.parametrize("heads,n", [(40, 3), (7, 150)])
+def test_append_layouts_and_many_heads(D, share, layout, heads, n):
+    """Every way of fetching rotary partners, rows of a token beyond one pass of a block; equal to rotating first."""
+    x, _ = rows_bf16(D + heads, n, 2 * heads, D)
+    k, v = x[:, :heads], x[:, heads:]
+    pos = torch.arange(n, dtype=torch.int32, device=torch_dev()) * 1237
+    slots = torch.arange(n, device=torch_dev()) * 2 + 1
+    rope = make_rope(D, int(D * share), layout, "none", 1.0)[0] if share else None
+    a, b = (empty_cache(-(-2 * n // 16) + 1, 16, heads, D) for _ in range(2))
+    a.append(k, v, slots, rope=rope, positions=pos)
+    kr = rope.apply(k, pos) if rope else k.contiguous()
+    codes = torch.empty((n * heads, D // 2), dtype=torch.uint8, device=torch_dev())
+    scales = torch.empty((n * heads, D // 32), dtype=torch.float16, device=torch_dev())
+    for i, rows in ((0, kr), (2, v.contiguous())):
+        S().strata_kv4_encode(rows, n * heads, D, codes, scales)
+        b.tensors[i][slots // 16, :, slots % 16] = codes.view(n, heads, -1)
+        b.tensors[i + 1][slots // 16, :, slots % 16] = scales.view(n, heads, -1)
+    for p, q in zip(a.tensors, b.tensors):
+        assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
 @pytest.mark.parametrize("rd,layout", [(2, "half"), (10, "half"), (6, "interleaved"), (24, "half")])
 def test_append_odd_rotary_widths(rd, layout):
     """Rotary widths that fill no chunks; equal to rotating first and encoding after."""
@@ -318,6 +342,33 @@ def test_attention_largest_scales(D, q_len):
     c = Case([(q_len, 257)], 4, 1, D, 16, q_gain=2.0**-14)
     for i in (1, 3):
         c.cache.tensors[i][::2] = 65504.0
+    c.check()
+
+
+@pytest.mark.parametrize("q_len", [1, 9])
+@pytest.mark.parametrize("n", [33, 65, 300, 1300])
+def test_attention_many_sequences(n, q_len):
+    """Batches beyond what one warp, and one block, looks over at once; some sequences idle, some without keys."""
+    r = np.random.default_rng(n)
+    seqs = [(int(q_len if r.random() < 0.8 else 0), int(r.integers(0, 120))) for _ in range(n)]
+    Case(seqs, 8, 1, 64, 16, seed=n).check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("hint", [0, 1, 6, 7, 1000])
+def test_attention_max_q_len_is_a_hint(D, hint):
+    """max_q_len chooses the kernel; longer and shorter runs of queries come out right under any."""
+    c = Case([(40, 333), (1, 270), (3, 3)], 8, 1, D, 32, window=200, seed=hint)
+    c.max_q = hint
+    c.check()
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 70])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+def test_attention_scales(q_len, scale):
+    """A negative scale, none at all, and one that leaves a single key."""
+    c = Case([(q_len, 500), (q_len, 90)], 8, 2, 128, 16, seed=7)
+    c.scale = scale
     c.check()
 
 
