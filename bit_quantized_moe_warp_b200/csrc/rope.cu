@@ -8,8 +8,8 @@
 // The kernel streams every row once (2 bytes in, 2 out per value) and is bound
 // by HBM. A block takes a few tokens at a time: their cosines and sines are
 // computed once (fp64, rotary_dim / 2 a token, one for each thread) into shared
-// memory and serve every head; a thread's first chunk is on its way meanwhile,
-// and later on the next one while a chunk is turned.
+// memory and serve every head; those of the block's next tokens are computed while
+// this one's chunks stream, and a chunk is fetched while the one before is turned.
 #include <cmath>
 #include <new>
 
@@ -44,7 +44,7 @@ __device__ __forceinline__ int quotient(int x, uint64_t inv) { return inv ? (int
 // values, so out may be x.
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a) {
-    __shared__ __align__(16) float2 cs[kThreads];  // [token][pair]
+    __shared__ __align__(16) float2 cs[2][kThreads];  // [token][pair], of this group of tokens and the next
     const int pairs = tab.rd / 2;
     const int rot = HALF ? tab.rd / 16 : tab.rd / 8;  // rotated items of a head
     struct Item {
@@ -52,7 +52,13 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ R
         __nv_bfloat16 *out;
         int c, t;
     };
-    for (int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block; t0 < a.n_tokens; t0 += (int64_t)gridDim.x * a.tokens_per_block) {
+    const int64_t step = (int64_t)gridDim.x * a.tokens_per_block;
+    const int lt = threadIdx.x / pairs, lp = threadIdx.x - lt * pairs;
+    auto angles = [&](int64_t t0, int b) {
+        if (lt < a.tokens_per_block && t0 + lt < a.n_tokens) cs[b][threadIdx.x] = rope_cs(tab, lp, a.positions[t0 + lt]);
+    };
+    int b = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block; t0 < a.n_tokens; t0 += step, b ^= 1) {
         const int nt = (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0);
         const int total = nt * a.heads * a.items;
         auto fetch = [&](Item &x, int it) {
@@ -70,9 +76,11 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ R
         Item cur, next;
         int it = threadIdx.x;
         if (it < total) fetch(next, it);
-        const int lt = threadIdx.x / pairs;
-        if (lt < nt) cs[threadIdx.x] = rope_cs(tab, threadIdx.x - lt * pairs, a.positions[t0 + lt]);
-        __syncthreads();
+        if (t0 == (int64_t)blockIdx.x * a.tokens_per_block) {
+            angles(t0, 0);
+            __syncthreads();
+        }
+        angles(t0 + step, b ^ 1);
         for (; it < total; it += kThreads) {
             cur = next;
             if (it + kThreads < total) fetch(next, it + kThreads);
@@ -81,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ R
                 continue;
             }
             // four or eight pairs, two for each 16-byte load
-            const float4 *c = reinterpret_cast<const float4 *>(cs + cur.t * pairs + cur.c * (HALF ? 8 : 4));
+            const float4 *c = reinterpret_cast<const float4 *>(cs[b] + cur.t * pairs + cur.c * (HALF ? 8 : 4));
             const uint32_t u[4] = {cur.u.x, cur.u.y, cur.u.z, cur.u.w};
             if constexpr (HALF) {
                 const uint32_t v[4] = {cur.v.x, cur.v.y, cur.v.z, cur.v.w};
@@ -110,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const __grid_constant__ R
                 *reinterpret_cast<uint4 *>(cur.out) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
-        __syncthreads();  // cs is written again
+        __syncthreads();  // the next group's angles are there, these are done with
     }
 }
 
@@ -247,7 +255,7 @@ extern "C" strata_status strata_rope_apply(strata_rope rope, const void *x, int6
         a.heads_inv = inverse(n_heads);
         a.items_inv = inverse(a.items);
         const int64_t blocks = (n_tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-        const int grid = (int)(blocks < 65536 ? blocks : 65536);
+        const int grid = (int)(blocks < 4 * 148 ? blocks : 4 * 148);  // four for each SM, each over several groups
         if (tab.half)
             k_rope_vec<true><<<grid, kThreads, 0, st>>>(tab, a);
         else
