@@ -124,8 +124,8 @@ struct AppendArgs {
 
 // What turns a key row: nothing, or pairs that one lane holds (the half layout
 // over the whole head: a chunk's partner is R / 2 runs on; the interleaved one),
-// or partners read once more from memory
-enum { kPlain, kHalfWhole, kInterleaved, kOther };
+// or partners read once more from memory, in whole chunks or one by one
+enum { kPlain, kHalfWhole, kInterleaved, kHalfChunks, kOther };
 
 // One block takes tokens_per_block tokens: their cosines and sines once
 // (fp64) into shared memory, while the first rows are on their way, then the key
@@ -209,6 +209,25 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
                         const uint32_t r0_ = pack_bf16(rope_first(u[0], u[1], c0), rope_second(u[0], u[1], c0));
                         const uint32_t r1_ = pack_bf16(rope_first(u[2], u[3], c1), rope_second(u[2], u[3], c1));
                         u[0] = bf16_lo(r0_), u[1] = bf16_hi(r0_), u[2] = bf16_lo(r1_), u[3] = bf16_hi(r1_);
+                    }
+                }
+            } else if constexpr (MODE == kHalfChunks) {
+#pragma unroll
+                for (int m = 0; m < R::kRuns; ++m) {
+                    const int c8 = 8 * (l + R::kLanes * m);
+                    if (c8 >= tab.rd) continue;
+                    const bool second = c8 >= pairs;
+                    const uint4 q4 = *reinterpret_cast<const uint4 *>(src + (second ? c8 - pairs : c8 + pairs));
+                    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+                    const float4 *c = reinterpret_cast<const float4 *>(ct + (second ? c8 - pairs : c8));
+                    const float sg = second ? 1.f : -1.f;  // u c - v s, v c + u s: a negated product rounds the same
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float4 k = c[e / 2];
+                        float *u = x[m] + e;
+                        const uint32_t w = pack_bf16(__fadd_rn(__fmul_rn(u[0], k.x), sg * __fmul_rn(bf16_lo(q[e / 2]), k.y)),
+                                                     __fadd_rn(__fmul_rn(u[1], k.z), sg * __fmul_rn(bf16_hi(q[e / 2]), k.w)));
+                        u[0] = bf16_lo(w), u[1] = bf16_hi(w);
                     }
                 }
             } else {
@@ -375,6 +394,7 @@ extern "C" strata_status strata_kv4_append(const strata_kv4_cache *cache, strata
     const int mode = tab.rd == 0                                    ? kPlain
                      : tab.half && tab.rd == cache->head_dim ? kHalfWhole
                      : !tab.half && tab.rd % 8 == 0          ? kInterleaved
+                     : tab.half && tab.rd % 16 == 0          ? kHalfChunks
                                                              : kOther;
     auto launch = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
@@ -384,6 +404,8 @@ extern "C" strata_status strata_kv4_append(const strata_kv4_cache *cache, strata
             k_kv4_append<D, kHalfWhole><<<(int)grid, kThreads, smem, st>>>(tab, a);
         else if (mode == kInterleaved)
             k_kv4_append<D, kInterleaved><<<(int)grid, kThreads, smem, st>>>(tab, a);
+        else if (mode == kHalfChunks)
+            k_kv4_append<D, kHalfChunks><<<(int)grid, kThreads, smem, st>>>(tab, a);
         else
             k_kv4_append<D, kOther><<<(int)grid, kThreads, smem, st>>>(tab, a);
     };
