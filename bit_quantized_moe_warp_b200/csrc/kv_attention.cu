@@ -41,6 +41,16 @@ namespace {
 // any mix of lengths fills the machine. A run that covers a sequence's whole
 // cache writes its rows; the others leave (M, l, O) in the workspace, two at
 // most for a CTA, and k_attn_join adds them up in a fixed order.
+//
+// Measured (B200, with the join, calls back to back): 1 token of 32 heads at
+// 131,072 cached tokens of 4 KV heads of 128 30.9 us (2.4 TB/s of the cache's
+// 75.5 MB), 64 sequences of 1,024 to 16,384 74 us (3.1 TB/s), 1 at 777 11 us.
+// About 10 us of each are fixed: three dependent loads (lengths, page table,
+// tile) before the first product, the join of the warps and of the CTAs. In the
+// stream itself 16 warps issue 2.4 to 3 of 4 instructions a cycle and SM, some
+// 740 for 32 keys (245 of them unpacking and adding up values).
+// 12 warps instead of 8 for 16 rows: no faster (51 and 54 us, 32 rows, 100,000
+// keys); 2 blocks of 128 registers for 16 rows of 64 values: the same.
 constexpr int kSplitParts = 2 * 16 * kSms;  // rows of partial results: 2 x 8 rows x 296 CTAs or 2 x 16 x 148
 constexpr int kSplitWarps = 8;
 // Rows of a KV head and sequence up to which k_attn_split is launched, 16 at a

@@ -131,7 +131,10 @@ enum { kPlain, kHalfWhole, kInterleaved, kHalfChunks, kOther };
 // (fp64) into shared memory, while the first rows are on their way, then the key
 // rows and the value rows of each (in this order, so that warps agree). Bound by
 // instruction issue: 7 butterflies, rotary and rounding of every value; values
-// go in pairs where the operation has a form for two.
+// go in pairs where the operation has a form for two. Measured: 8,192 tokens of
+// 4 heads of 128 14.3 us (1.5 TB/s, 37 instructions a value, issue 57 %), without
+// rotary 12.1 us; 64 tokens 7.7 us a call, the call's own cost. At 64 registers
+// and 4 blocks for an SM: 16.5 us.
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__ RopeTable tab,
                                                         const __grid_constant__ AppendArgs a) {
@@ -300,6 +303,8 @@ struct CopyArgs {
     uint32_t code_vecs, scale_vecs;  // 16-byte words of a page in a code / scale plane
 };
 
+// Bound by HBM: 400 pages of 37 KB in 48 caches 239 us (5.9 TB/s of 2 x 708 MB),
+// 8 pages 7.8 us a call.
 template <int PAIRS>
 __global__ void __launch_bounds__(kThreads) k_kv4_copy(const __grid_constant__ CopyArgs<PAIRS> a) {
     const int64_t n = (int64_t)a.n_caches * a.n_pairs * 4;

@@ -145,9 +145,12 @@ strata_status strata_kv4_copy_pages(const strata_kv4_cache *caches, int32_t n_ca
  * q passes through `rope` first (NULL: none) at positions[t]; here the rotated
  * row is kept in fp32 instead of being rounded to bf16.
  * Precision: logits, softmax statistics and output sums in fp32; the rotated
- * q, the values and the probabilities enter the tensor cores in fp16 (with
- * power-of-two scales, so that no magnitude of the inputs overflows). Results
- * do not depend on timing: the same call gives the same bits.
+ * q, the probabilities (times the values' scales, or beside scaled values) and,
+ * with more than 48 rows max_q_len * n_q_heads / n_kv_heads, the scaled keys
+ * enter the tensor cores in fp16 (with power-of-two scales, so that no
+ * magnitude of the inputs overflows); the queries' cosines and sines are those
+ * of the hardware (2^-20.9). Results do not depend on timing: the same call
+ * gives the same bits, another max_q_len may give others.
  * Any n_seqs and lengths >= 0; q and out 16-byte aligned, token strides
  * multiples of 8, heads head_dim apart.
  * workspace: strata_kv4_attention_workspace_bytes() bytes, 16-byte aligned,
@@ -166,7 +169,9 @@ typedef struct {
 } strata_kv4_attn_desc;
 
 /* Workspace of strata_kv4_attention on this cache's shape for n_q_heads query
- * heads, whatever the sequences; 0 for shapes that are not supported. */
+ * heads, whatever the sequences (partial results of 148 thread blocks: 21 MB
+ * for head_dim 64, 40 MB for 128 and 256); 0 for shapes that are not supported.
+ * A model's layers, one after the other, can share one. */
 size_t strata_kv4_attention_workspace_bytes(const strata_kv4_cache *cache, int32_t n_q_heads);
 
 strata_status strata_kv4_attention(const strata_kv4_cache *cache, const strata_kv4_attn_desc *desc, strata_rope rope,
