@@ -699,7 +699,7 @@ cudaError_t launch_split(const RopeTable &tab, const AttnArgs &a, cudaStream_t s
     const cudaError_t e = allow_smem(k_attn_split<D, NT>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     const cudaError_t l = launch_early(k_attn_split<D, NT>, dim3(C::CTAS), kSplitWarps * 32, C::SMEM, st, tab, a);
-    return l != cudaSuccess ? l : launch_join<D, C::ROWS, 8, false>(a, C::CTAS, st);
+    return l != cudaSuccess ? l : launch_join<D, C::ROWS, false>(a, C::CTAS, st);
 }
 
 }  // namespace

@@ -85,17 +85,15 @@ struct Span {  // what k_attn_join needs of the last piece of a CTA
     int pad[2];
 };
 
-// One block for each piece that several CTAs share and 16 / WPR of its query
-// rows at a time: WPR warps over the parts of a row, each with a running
-// maximum of its own, then over each other, in a fixed order. Few rows of many
-// parts take 8 warps, many rows of few parts 1. Bound by the latency of its two
-// dependent loads, the span and the parts.
-// PLANES: a part's rows lie in planes of four values, [D / 4 + 1][ROWS] float4,
-// else as [ROWS][D + 4] floats; M and l follow the D values.
-template <int D, int ROWS, int WPR, bool PLANES>
+// One block for each piece that several CTAs share and two of its query rows at
+// a time: 8 warps over the parts of a row ([ROWS][D + 4] floats, M and l behind
+// the values), each with a running maximum of its own, then over each other, in
+// a fixed order. Bound by the latency of its two dependent loads, the span and
+// the parts.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnArgs a) {
     constexpr int P = D / 32, PART = D + 4, BATCH = P == 8 ? 2 : 4;
-    constexpr int RPB = 16 / WPR;
+    constexpr int WPR = 8, RPB = 16 / WPR;
     __shared__ float so[WPR][RPB][D], sl[WPR][RPB], sm[WPR][RPB];
     griddep_launch_dependents();
     griddep_wait();
@@ -121,7 +119,7 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
                 for (int j = 0; j < P; ++j) w[k][j] = 0.f;
                 if (i >= sp.parts) continue;
                 const float *p = parts + (int64_t)((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * (ROWS * PART);
-                auto at = [&](int d) { return PLANES ? p + ((d >> 2) * ROWS + r) * 4 + (d & 3) : p + r * PART + d; };
+                auto at = [&](int d) { return p + r * PART + d; };
                 ml[k] = *reinterpret_cast<const float2 *>(at(D));
                 if constexpr (P == 2) *reinterpret_cast<float2 *>(w[k]) = *reinterpret_cast<const float2 *>(at(lane * P));
                 if constexpr (P >= 4)
@@ -145,30 +143,86 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnA
                 for (int j = 0; j < P; ++j) v[j] = fmaf(w[k][j], g, v[j]);
             }
         }
-        if constexpr (WPR > 1) {
 #pragma unroll
-            for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
-            if (lane == 0) sl[wq][wr] = sum, sm[wq][wr] = m;
-            __syncthreads();
-            if (wq == 0) {
-                float top = m;
+        for (int j = 0; j < P; ++j) so[wq][wr][lane * P + j] = v[j];
+        if (lane == 0) sl[wq][wr] = sum, sm[wq][wr] = m;
+        __syncthreads();
+        if (wq == 0) {
+            float top = m;
 #pragma unroll
-                for (int w = 1; w < WPR; ++w) top = fmaxf(top, sm[w][wr]);
-                const float f = ex2(m - top);
-                sum *= f;
+            for (int w = 1; w < WPR; ++w) top = fmaxf(top, sm[w][wr]);
+            const float f = ex2(m - top);
+            sum *= f;
 #pragma unroll
-                for (int j = 0; j < P; ++j) v[j] *= f;
+            for (int j = 0; j < P; ++j) v[j] *= f;
 #pragma unroll
-                for (int w = 1; w < WPR; ++w) {
-                    const float g = ex2(sm[w][wr] - top);
-                    sum = fmaf(sl[w][wr], g, sum);
+            for (int w = 1; w < WPR; ++w) {
+                const float g = ex2(sm[w][wr] - top);
+                sum = fmaf(sl[w][wr], g, sum);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) v[j] = fmaf(so[w][wr][lane * P + j], g, v[j]);
-                }
+                for (int j = 0; j < P; ++j) v[j] = fmaf(so[w][wr][lane * P + j], g, v[j]);
             }
         }
         if (wq == 0 && live) store_row<D>(a, v, sum, sp.t0, sp.hk, sp.row0 + r, lane);
-        if constexpr (WPR > 1) __syncthreads();
+        __syncthreads();
+    }
+}
+
+// The same for parts in planes of four values over the rows, [D / 4 + 1][ROWS]
+// float4: many rows of few parts. A thread adds up one float4 of a row, so that
+// a warp's loads lie together; then a warp takes a row for the transform.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(512) k_attn_join_planes(const __grid_constant__ AttnArgs a) {
+    constexpr int P = D / 32, RPB = 2048 / D;  // rows of a block: one float4 for each thread
+    __shared__ float so[RPB][D], sl[RPB];
+    griddep_launch_dependents();
+    griddep_wait();
+    const Span sp = static_cast<const Span *>(a.workspace)[blockIdx.x];
+    if (sp.parts == 0) return;
+    const float4 *parts = reinterpret_cast<const float4 *>(static_cast<const Span *>(a.workspace) + kSplitMaxCtas);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tr = threadIdx.x % RPB, plane = threadIdx.x / RPB;
+    for (int r0 = RPB * blockIdx.y; r0 < sp.rows; r0 += RPB * gridDim.y) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f, m = -FLT_MAX;
+        const int r = min(r0 + tr, sp.rows - 1);
+        for (int i0 = 0; i0 < sp.parts; i0 += 4) {
+            float4 w[4], ml[4];
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                ml[k] = make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
+                const int i = i0 + k;
+                if (i >= sp.parts) continue;
+                const float4 *p = parts + (int64_t)((blockIdx.x + i) * 2 + (i ? 0 : sp.slot)) * (ROWS * (D / 4 + 1)) + r;
+                ml[k] = p[(D / 4) * ROWS];
+                w[k] = p[plane * ROWS];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+            const float f = ex2(m - top);
+            m = top;
+            sum *= f;
+            v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float g = ex2(ml[k].x - m);
+                sum = fmaf(ml[k].y, g, sum);
+                v.x = fmaf(w[k].x, g, v.x), v.y = fmaf(w[k].y, g, v.y);
+                v.z = fmaf(w[k].z, g, v.z), v.w = fmaf(w[k].w, g, v.w);
+            }
+        }
+        *reinterpret_cast<float4 *>(&so[tr][plane * 4]) = v;
+        if (plane == 0) sl[tr] = sum;
+        __syncthreads();
+        for (int k = warp; k < RPB && r0 + k < sp.rows; k += 16) {
+            float x[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) x[j] = so[k][lane * P + j];
+            store_row<D>(a, x, sl[k], sp.t0, sp.hk, sp.row0 + r0 + k, lane);
+        }
+        __syncthreads();
     }
 }
 
@@ -202,12 +256,15 @@ cudaError_t allow_smem(Kernel *kernel, int bytes, std::atomic<uint64_t> &done) {
     return e;
 }
 
-template <int D, int ROWS, int WPR, bool PLANES>
+template <int D, int ROWS, bool PLANES>
 cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
     const int64_t rows = (int64_t)a.d.max_q_len * a.group;  // a hint only: a block takes more rows in turn
-    constexpr int RPB = 16 / WPR;
+    constexpr int RPB = PLANES ? 2048 / D : 2;
     const unsigned y = rows < 1 ? 1 : rows < ROWS ? (unsigned)(rows + RPB - 1) / RPB : ROWS / RPB;
-    return launch_early(k_attn_join<D, ROWS, WPR, PLANES>, dim3(ctas, y), 512, 0, st, a);
+    if constexpr (PLANES)
+        return launch_early(k_attn_join_planes<D, ROWS>, dim3(ctas, y), 512, 0, st, a);
+    else
+        return launch_early(k_attn_join<D, ROWS>, dim3(ctas, y), 512, 0, st, a);
 }
 
 // Many query rows (kv_attn_tiles.cu): bytes of its partial results, and the launch

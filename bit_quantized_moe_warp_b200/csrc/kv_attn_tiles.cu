@@ -25,7 +25,7 @@
 // as a factor of its scores, the value's as an exponent added to x.
 //
 // Work: the key tiles of all items in a row, cut into 148 equal runs, one for
-// each CTA; pieces of an item that several CTAs share go through k_attn_join.
+// each CTA; pieces of an item that several CTAs share go through k_attn_join_planes.
 //
 // Measured (B200): 8,192 tokens of 32 heads of 128, the last of 32,768 (4 KV
 // heads): 4.55 ms, 846 TFLOP/s. A step of 256 rows and 128 keys takes about
@@ -990,7 +990,7 @@ cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
     const cudaError_t e = allow_smem(k_attn_tiles<D>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     const cudaError_t l = launch_early(k_attn_tiles<D>, dim3(kSms), kThreads, C::SMEM, st, tab, a);
-    return l != cudaSuccess ? l : launch_join<D, C::ROWS, 1, true>(a, kSms, st);
+    return l != cudaSuccess ? l : launch_join<D, C::ROWS, true>(a, kSms, st);
 }
 
 }  // namespace
