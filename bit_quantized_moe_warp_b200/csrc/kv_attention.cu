@@ -157,9 +157,11 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_gro
     s.groups = (int)(((int64_t)s.n * a.group + rows_per_group - 1) / rows_per_group);
     return s;
 }
-// units of one (KV head, row group); one at least, which writes the zeros of a
-// sequence without keys
-__device__ __forceinline__ int seq_units(const Seq &s) { return max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
+// units of one (KV head, row group): those that stand for what a piece of it
+// costs besides its tiles (rows in, warps joined, results out), then its tiles;
+// one at least, which writes the zeros of a sequence without keys
+constexpr int kSplitHead = 2;
+__device__ __forceinline__ int seq_units(const Seq &s) { return kSplitHead + max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
@@ -287,16 +289,19 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
     const uint32_t ring_u = smem_u32(ring), scratch_u = smem_u32(scratch);
     const uint32_t lane_chunk = code_chunk<D>(lane / NB, lane % NB);
 
+    int count = 0;  // pieces
     for (int u = 0; u < units;) {
         const int u_end = min(first + per, units);
+        const int t_lo = max(u - first - kSplitHead, 0), t_hi = u_end - first - kSplitHead;
+        if (t_hi <= t_lo) break;  // the run ends before the first tile
         const int rg = vh / a.c.n_kv_heads, hk = vh - rg * a.c.n_kv_heads;
         const int row0 = rg * ROWS;
         const int rows = min(ROWS, s.n * a.group - row0);
         const int p_first = s.L - s.n;           // position of query 0
 
         // ---- the warp's tiles: tile0 + 8 unit + warp
-        int it = s.tile0 + (u - first) * kSplitWarps + warp;
-        const int t_end = min(s.tile0 + s.tiles, s.tile0 + (u_end - first) * kSplitWarps);
+        int it = s.tile0 + t_lo * kSplitWarps + warp;
+        const int t_end = min(s.tile0 + s.tiles, s.tile0 + t_hi * kSplitWarps);
         const int32_t *table = a.table + (int64_t)b * a.d.max_pages;
         int nit = it;                            // next tile to ask for
         uint32_t page[2] = {~0u, ~0u}, there = 0;  // the pages of its halves; bit 2 s + h: half h of stage s is there
@@ -643,8 +648,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                         make_float4(o[n][2 * k][j], o[n][2 * k][j + 2], o[n][2 * k + 1][j], o[n][2 * k + 1][j + 2]);
             }
         __syncthreads();
-        const bool whole = u == first && u_end == first + per;
-        const int slot = u ? 1 : 0;
+        const bool whole = t_lo == 0 && u_end == first + per;
+        const int slot = count ? 1 : 0;  // the first piece may go on from the CTA before, the last one into the next
         for (int r = warp; r < rows; r += kSplitWarps) {
             float m = sM[r];
 #pragma unroll
@@ -669,7 +674,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                 if (lane == 0) part[D] = m, part[D + 1] = sum;
             }
         }
-        if (u == first && !whole && threadIdx.x == 0) {
+        if (t_lo == 0 && !whole && threadIdx.x == 0) {
             // it starts here and ends in the CTA that holds its last unit
             const int64_t last = u_lo + first + per - 1;
             int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
@@ -678,6 +683,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
         }
         __syncthreads();
         u = u_end;
+        ++count;
         if (u < units) {
             first += per;
             if (++vh == s.groups * a.c.n_kv_heads) {

@@ -24,8 +24,8 @@
 // normalised by its own power of two, which the softmax takes back: the key's
 // as a factor of its scores, the value's as an exponent added to x.
 //
-// Work: the key tiles of all items in a row, cut into 148 equal runs, one for
-// each CTA; pieces of an item that several CTAs share go through k_attn_join_planes.
+// Work: the key tiles of all items in a row, each item with kHead units in front,
+// cut into 148 equal runs, one for each CTA; pieces of an item that several CTAs share go through k_attn_join_planes.
 //
 // Measured (B200): 8,192 tokens of 32 heads of 128, the last of 32,768 (4 KV
 // heads): 4.55 ms, 846 TFLOP/s. A step of 256 rows and 128 keys takes about
@@ -226,8 +226,11 @@ STRATA_DEV Item item_of(const AttnArgs &a, const SeqBase &s, int rt) {
     it.tiles = (int)(((int64_t)hi + C::TK - 1) / C::TK) - it.tile0;
     return it;
 }
-// units of an item; one at least, which writes the zeros of rows without keys
-STRATA_DEV int item_units(const Item &it) { return max(it.tiles, 1); }
+// Units of an item: those that stand for what a piece of it costs besides its
+// tiles (rows in, results out), then its tiles; one at least, which writes the
+// zeros of rows without keys.
+constexpr int kHead = 8;
+STRATA_DEV int item_units(const Item &it) { return kHead + max(it.tiles, 1); }
 
 // A run of a CTA's key tiles inside one item, and what came before it
 struct Piece {
@@ -238,6 +241,10 @@ struct Piece {
     bool whole, dual, after_dual;
     uint32_t tc, sc[2], count;  // key tiles, steps in each S, pieces so far: buffers and phases
 };
+
+// Where a CTA leaves a partial result: its first piece may go on from the CTA
+// before it, its last one into the next
+STRATA_DEV int slot_of(const Piece &p) { return p.count ? 1 : 0; }
 
 STRATA_DEV int item_count(const AttnArgs &a, int n, int rows) { return (int)(((int64_t)n * a.group + rows - 1) / rows); }
 
@@ -417,20 +424,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; p.u < units;) {
         const int per = item_units(p.it);
         p.u_end = min(p.first + per, units);
-        p.whole = p.u == p.first && p.u_end == p.first + per;
-        p.kt0 = p.it.tile0 + (p.u - p.first);
-        p.nt = min(p.u_end - p.u, p.it.tile0 + p.it.tiles - p.kt0);  // 0: rows without keys
+        const int t_lo = max(p.u - p.first - kHead, 0), t_hi = p.u_end - p.first - kHead;
+        if (t_hi <= t_lo) break;  // the run ends before the item's first tile
+        p.whole = t_lo == 0 && p.u_end == p.first + per;
+        p.kt0 = p.it.tile0 + t_lo;
+        p.nt = min(t_hi, p.it.tiles) - t_lo;  // 0: rows without keys
         p.dual = SLOTS == 2 && p.it.rows <= 128;
         p.steps = SLOTS == 2 && !p.dual ? 2 * p.nt : p.nt;
 
         if (!role(p)) break;
         // ---- the next piece
-        if (p.u == p.first && !p.whole && threadIdx.x == 0) {
+        if (t_lo == 0 && !p.whole && threadIdx.x == 0) {
             // it starts here and ends in the CTA that holds its last unit
             const int64_t last = u_lo + p.first + per - 1;
             int c = (int)run_start(ctas, last, total);  // run c starts at `last` or before it
             while (run_start(total, c + 1, ctas) <= last) ++c;
-            spans[blockIdx.x] = Span{c - (int)blockIdx.x + 1, p.u ? 1 : 0, (int)p.s.t0, p.it.rows, p.hk, p.it.row0, {0, 0}};
+            spans[blockIdx.x] = Span{c - (int)blockIdx.x + 1, slot_of(p), (int)p.s.t0, p.it.rows, p.hk, p.it.row0, {0, 0}};
         }
         p.tc += p.nt;
         if (SLOTS == 2)
@@ -958,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         // planes of four values over the rows: the lanes' stores lie together
-                        float4 *part = reinterpret_cast<float4 *>(parts + (int64_t)(blockIdx.x * 2 + (p.u ? 1 : 0)) * C::ROWS * C::PART) + r;
+                        float4 *part = reinterpret_cast<float4 *>(parts + (int64_t)(blockIdx.x * 2 + slot_of(p)) * C::ROWS * C::PART) + r;
 #pragma unroll 1
                         for (int g = 0; g < D / 32; ++g) {
                             float x[32];
