@@ -43,8 +43,8 @@ namespace {
 // most for a CTA, and k_attn_join adds them up in a fixed order.
 //
 // Measured (B200, with the join, calls back to back): 1 token of 32 heads at
-// 131,072 cached tokens of 4 KV heads of 128 30.9 us (2.4 TB/s of the cache's
-// 75.5 MB), 64 sequences of 1,024 to 16,384 74 us (3.1 TB/s), 1 at 777 11 us.
+// 131,072 cached tokens of 4 KV heads of 128 30.8 us (2.4 TB/s of the cache's
+// 75.5 MB), 64 sequences of 1,024 to 16,384 69 us (3.3 TB/s), 1 at 777 11 us.
 // About 10 us of each are fixed: three dependent loads (lengths, page table,
 // tile) before the first product, the join of the warps and of the CTAs. In the
 // stream itself 16 warps issue 2.4 to 3 of 4 instructions a cycle and SM, some
@@ -160,6 +160,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_gro
 // units of one (KV head, row group): those that stand for what a piece of it
 // costs besides its tiles (rows in, warps joined, results out), then its tiles;
 // one at least, which writes the zeros of a sequence without keys
+// us with 0, 1, 2, 4: 64 sequences up to 16,384 74.5, 70.1, 69.4, 74.0; 8 of 6
+// tokens up to 32,768 58.6, 55.1, 53.6, 53.3; 64 up to 1,500 23, 20, 20, 21.7.
 constexpr int kSplitHead = 2;
 __device__ __forceinline__ int seq_units(const Seq &s) { return kSplitHead + max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }
 
