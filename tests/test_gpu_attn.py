@@ -372,6 +372,56 @@ def test_attention_scales(q_len, scale):
     c.check()
 
 
+@pytest.mark.parametrize("q_len", [1, 5, 80])
+@pytest.mark.parametrize("page", [128, 1024])
+def test_attention_large_pages(page, q_len):
+    Case([(q_len, 2500), (q_len, 100), (q_len, 1024)], 8, 2, 128, page, window=1500, seed=page).check()
+
+
+@pytest.mark.parametrize("q_len", [1, 70])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_attention_far_and_negative_positions(q_len, layout):
+    """Positions are the caller's: any int32, whatever the place in the cache."""
+    c = Case([(q_len, 200), (q_len, 90)], 8, 2, 128, 16)
+    n = c.q.shape[0]
+    pos = np.random.default_rng(3).integers(-(2**31), 2**31, n).astype(np.int32)
+    pos[0], pos[-1] = 2**31 - 1, -(2**31)
+    c.rope, (f, m) = make_rope(128, 128, layout, "none", 1.0)
+    c.positions = torch.from_numpy(pos).to(torch_dev())
+    cs = [torch.from_numpy(t).double().to(torch_dev())[:, None] for t in R.rope_cs(pos, f, m)]
+    iu = torch.arange(64, device=torch_dev()) * (1 if layout == "half" else 2)
+    iv = iu + (64 if layout == "half" else 1)
+    u, v = c.q64[..., iu].clone(), c.q64[..., iv].clone()
+    c.q64[..., iu], c.q64[..., iv] = u * cs[0] - v * cs[1], v * cs[0] + u * cs[1]
+    c.check()
+
+
+def test_attention_from_several_threads():
+    """Calls from four threads, a stream and a workspace each, on one cache."""
+    import threading
+    dev = torch_dev()
+    cases = [Case([(q, 1500), (q, 300)], 16, 2, 128, 64, seed=20 + q) for q in (1, 2, 5, 60)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w):
+        with torch.cuda.device(dev), torch.cuda.stream(torch.cuda.Stream(dev)):
+            ws, o = c.cache.attention_workspace(16), torch.zeros_like(w)
+            for _ in range(30):
+                c.run(o, workspace=ws)
+            torch.cuda.current_stream().synchronize()
+            if not torch.equal(o.view(torch.int16), w.view(torch.int16)):
+                bad.append(c.max_q)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_attention_long_context_offsets():
     """One sequence over 200,000 tokens; and a pool whose byte offsets pass 32 bits, used at its far end."""
     Case([(1, 200_003)], 8, 1, 128, 64, seed=3).check()
