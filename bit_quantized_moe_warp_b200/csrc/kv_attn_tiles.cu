@@ -766,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t ff = pack2(f, f);
                     sum[0] = fma2(sum[0], ff, 0), sum[1] = fma2(sum[1], ff, 0);
                     const __half2 fh = __float2half2_rn(f);
+                    tmem_st_wait();  // what this step has stored so far is read back
 #pragma unroll 1
                     for (int h = 0; h < g; ++h) {
                         float y[16];
@@ -840,6 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             move(largest(w) * fac, g);
                             weigh(w, w, fac);
                             pack(w, y);
+                            // anew: registers that a load is still filling must not be kept over all this
+                            if (g + 1 < TK / 32) tmem_ld32(scol + 32 * g + 32, xa);
                         }
                         tmem_st16(scol + 16 * g, y);  // columns that were read before
                         add(w);
