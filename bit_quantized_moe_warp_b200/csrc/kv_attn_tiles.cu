@@ -48,7 +48,10 @@ namespace {
 
 constexpr int kThreads = 20 * 32;  // the last three warps only complete a group of four
 constexpr int kMmaWarp = 16;
-constexpr int kInfo = 4;  // tiles whose flags are kept
+// Tiles whose flags are kept. Those of tile c are written ahead of the wait for its
+// buffer, once that for c - 1 has ended: the product of c - 3 is done, so c - 5 is
+// weighed, and c - 4 may be at it still.
+constexpr int kInfo = 8;
 
 template <int D>
 struct Tiles {

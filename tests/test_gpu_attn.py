@@ -372,6 +372,20 @@ def test_attention_scales(q_len, scale):
     c.check()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [40, 180, 333])
+def test_attention_maximum_moves_inside_a_tile(D, window):
+    """Queries whose window begins inside a tile: their maximum moves after parts of the tile, and of earlier tiles,
+    have been weighed; the same bits every time."""
+    c = Case([(16, 600 + 37 * i) for i in range(40)], 16, 4, D, 32, window=window, seed=window)
+    c.max_q = 1000  # the kernel for many rows
+    first = c.check()
+    for _ in range(5):
+        out = torch.zeros_like(c.q)
+        c.run(out)
+        assert torch.equal(out.view(torch.int16), first.contiguous().view(torch.int16))
+
+
 @pytest.mark.parametrize("q_len", [1, 5, 80])
 @pytest.mark.parametrize("page", [128, 1024])
 def test_attention_large_pages(page, q_len):
