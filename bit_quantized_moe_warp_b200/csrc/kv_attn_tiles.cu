@@ -840,12 +840,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t m = h2_bits(__hmax2(__hmax2(t[0], t[1]), __hmax2(t[2], t[3])));
                         if (__any_sync(kFullMask, max(m >> 16, m & 0xffffu) > 0x6800u)) {  // 2^11
                             tmem_ld32(scol + 32 * g, w);
-                            tmem_ld_wait();
+                            tmem_ld_wait();  // ends the load ahead too
                             move(largest(w) * fac, g);
                             weigh(w, w, fac);
                             pack(w, y);
-                            // anew: registers that a load is still filling must not be kept over all this
-                            if (g + 1 < TK / 32) tmem_ld32(scol + 32 * g + 32, xa);
                         }
                         tmem_st16(scol + 16 * g, y);  // columns that were read before
                         add(w);
