@@ -28,7 +28,7 @@
 // cut into 148 equal runs, one for each CTA; pieces of an item that several CTAs share go through k_attn_join_planes.
 //
 // Measured (B200): 8,192 tokens of 32 heads of 128, the last of 32,768 (4 KV
-// heads): 4.55 ms, 846 TFLOP/s. A step of 256 rows and 128 keys takes about
+// heads): 4.52 ms, 851 TFLOP/s. A step of 256 rows and 128 keys takes about
 // 5,000 cycles, of which the tensor cores work 2,080 (ncu: 28 % of all cycles in
 // a smaller call) and the exponentials need 2,048: a chain of product, wait,
 // softmax (2,500 for a half, two halves at once), wait and product, with two
