@@ -8,6 +8,7 @@ loudly when the shared library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -150,6 +151,18 @@ def _stream(stream, device=None):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _making_on(stream, device):
+    """Context for what a call allocates itself: it belongs to the stream that the call's kernels run on, so that a
+    fill comes before them, and a block given back on return goes to nobody who does not come after them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _host_i32(v):
@@ -492,12 +505,14 @@ class Rope:
             pass
 
     def apply(self, x, positions, out=None, stream=None):
-        """x [tokens, heads, head_dim] bf16 (any token and head strides), positions int32 [tokens]; out may be x."""
+        """x [tokens, heads, head_dim] bf16 (any token and head strides), positions int32 [tokens]; out may be x.
+        An `out` that the call makes belongs to `stream`, like any tensor made under torch.cuda.stream."""
         import torch
         n, heads, D = x.shape
-        if out is None:
-            out = torch.empty((n, heads, D), dtype=x.dtype, device=x.device)
         dev = x.get_device()
+        if out is None:
+            with _making_on(stream, dev):
+                out = torch.empty((n, heads, D), dtype=x.dtype, device=x.device)
         _need(x, "x", torch.bfloat16, dev)
         _need(out, "out", torch.bfloat16, dev)
         _need(positions, "positions", torch.int32, dev)
@@ -577,12 +592,15 @@ class Kv4Cache:
                   positions=None, workspace=None, stream=None):
         """Causal attention of q [tokens, heads, head_dim] bf16 (any token stride). Sequence b: query rows
         q_offsets[b] .. q_offsets[b + 1] - 1, the last of its kv_lens[b] cached tokens, on pages block_table[b]
-        (all int32); max_q_len its longest query run. Rows outside every sequence stay as they are in `out`."""
+        (all int32); max_q_len its longest query run. Rows outside every sequence stay as they are in `out`. Without
+        `out` the call makes one of zeros; it, and a workspace that the call makes, belong to `stream`, like any
+        tensor made under torch.cuda.stream."""
         import torch
         n, heads, D = q.shape
         dev = self.index
         if out is None:
-            out = torch.zeros((n, heads, D), dtype=q.dtype, device=self.device)
+            with _making_on(stream, dev):
+                out = torch.zeros((n, heads, D), dtype=q.dtype, device=self.device)
         _need(q, "q", torch.bfloat16, dev)
         _need(out, "out", torch.bfloat16, dev)
         for name, t in (("q_offsets", q_offsets), ("kv_lens", kv_lens), ("block_table", block_table)):
@@ -606,7 +624,8 @@ class Kv4Cache:
                 raise ValueError(f"positions {tuple(positions.shape)}")
             handle, where = rope.handle, positions.data_ptr()
         if workspace is None:
-            workspace = self.attention_workspace(heads)
+            with _making_on(stream, dev):
+                workspace = self.attention_workspace(heads)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"the workspace is on {workspace.device}, not contiguous on GPU {dev}")
         desc = strata_kv4_attn_desc(B, heads, max_q_len, block_table.shape[1], n, qt, ot, window,
