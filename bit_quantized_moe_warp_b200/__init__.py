@@ -477,6 +477,21 @@ def _need(t, name, dtype, device):
         raise ValueError(f"{name} is on {t.device}, not on {f'GPU {device}' if device >= 0 else 'a GPU'}")
 
 
+def _rotary(rope, positions, n, device):
+    """Handle of a Rope and address of its rows' positions; (None, None), the library's "no rotation", without one."""
+    if rope is None:
+        return None, None
+    if rope.handle is None:
+        raise ValueError("the Rope is closed")
+    if positions is None:
+        raise ValueError("rope needs positions")
+    import torch
+    _need(positions, "positions", torch.int32, device)
+    if positions.shape != (n,) or not positions.is_contiguous():
+        raise ValueError(f"positions {tuple(positions.shape)}")
+    return rope.handle, positions.data_ptr()
+
+
 class Rope:
     """Rotary positions of head rows: the table of frequencies (include/strata_attn.h)."""
 
@@ -508,6 +523,8 @@ class Rope:
         """x [tokens, heads, head_dim] bf16 (any token and head strides), positions int32 [tokens]; out may be x.
         An `out` that the call makes belongs to `stream`, like any tensor made under torch.cuda.stream."""
         import torch
+        if self.handle is None:
+            raise ValueError("the Rope is closed")
         n, heads, D = x.shape
         dev = x.get_device()
         if out is None:
@@ -569,14 +586,7 @@ class Kv4Cache:
         (kt, kh, k1), (vt, vh, v1) = k.stride(), v.stride()
         if n and ((kh, k1) != (D, 1) or (vh, v1) != (D, 1) or not slots.is_contiguous()):
             raise ValueError("the heads of a token and the slots must be contiguous")
-        handle = where = None
-        if rope is not None:
-            if positions is None:
-                raise ValueError("rope needs positions")
-            _need(positions, "positions", torch.int32, dev)
-            if positions.shape != (n,) or not positions.is_contiguous():
-                raise ValueError(f"positions {tuple(positions.shape)}")
-            handle, where = rope.handle, positions.data_ptr()
+        handle, where = _rotary(rope, positions, n, dev)
         _on(dev, _lib.strata_kv4_append, self._desc, handle, k.data_ptr(), kt, v.data_ptr(), vt, where, slots.data_ptr(),
             n, _stream(stream, dev))
 
@@ -615,14 +625,7 @@ class Kv4Cache:
         (qt, qh, q1), (ot, oh, o1) = q.stride(), out.stride()
         if n and ((qh, q1) != (D, 1) or (oh, o1) != (D, 1)):
             raise ValueError("the heads of a token must be contiguous")
-        handle = where = None
-        if rope is not None:
-            if positions is None:
-                raise ValueError("rope needs positions")
-            _need(positions, "positions", torch.int32, dev)
-            if positions.shape != (n,) or not positions.is_contiguous():
-                raise ValueError(f"positions {tuple(positions.shape)}")
-            handle, where = rope.handle, positions.data_ptr()
+        handle, where = _rotary(rope, positions, n, dev)
         if workspace is None:
             with _making_on(stream, dev):
                 workspace = self.attention_workspace(heads)

@@ -144,3 +144,17 @@ def test_buffers_are_made_on_the_stream_of_the_call(rig, stream, handle):
     assert name == "strata_rope_apply" and args[-1] == handle and args[7] == out.data_ptr()
     assert rig.made == [out] and out.stream == handle
     assert rig.current == [CURRENT]
+
+
+def test_closed_rope_is_refused(rig):
+    """The library reads a missing rotary handle as no rotation: a closed one must not pass for that."""
+    rope, cache = rig.S.Rope(128), rig.cache()
+    rope.close()
+    with pytest.raises(ValueError, match="closed"):
+        cache.append(rig.bf16(3, 2, 128), rig.bf16(3, 2, 128), Tensor((3,), torch.int64), rope=rope, positions=rig.i32(3))
+    with pytest.raises(ValueError, match="closed"):
+        cache.attention(rig.bf16(3, 8, 128), rig.i32(3), rig.i32(2), rig.i32(2, 2), max_q_len=2, rope=rope,
+                        positions=rig.i32(3))
+    with pytest.raises(ValueError, match="closed"):
+        rope.apply(rig.bf16(3, 8, 128), rig.i32(3))
+    assert not rig.calls
