@@ -477,6 +477,13 @@ def _need(t, name, dtype, device):
         raise ValueError(f"{name} is on {t.device}, not on {f'GPU {device}' if device >= 0 else 'a GPU'}")
 
 
+def _int32(v, name):
+    """v, if a 32-bit field of the library's structures holds it: ctypes would keep the low bits of a wider one."""
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name} {v} is not an int32")
+    return v
+
+
 def _rotary(rope, positions, n, device):
     """Handle of a Rope and address of its rows' positions; (None, None), the library's "no rotation", without one."""
     if rope is None:
@@ -503,9 +510,11 @@ class Rope:
                  original_max_position=0, beta_fast=0.0, beta_slow=0.0, attn_factor=0.0):
         self.handle = None
         self.head_dim = head_dim
-        self.desc = strata_rope_desc(head_dim, head_dim if rotary_dim is None else rotary_dim,
+        self.desc = strata_rope_desc(_int32(head_dim, "head_dim"),
+                                     _int32(head_dim if rotary_dim is None else rotary_dim, "rotary_dim"),
                                      self.LAYOUTS.get(layout, -1), self.SCALINGS.get(scaling, -1), theta, factor,
-                                     original_max_position, beta_fast, beta_slow, attn_factor)
+                                     _int32(original_max_position, "original_max_position"), beta_fast, beta_slow,
+                                     attn_factor)
         self.handle = strata_rope_create(self.desc)
 
     def close(self):
@@ -593,7 +602,7 @@ class Kv4Cache:
     def attention_workspace(self, n_q_heads):
         """A workspace for attention() with n_q_heads query heads, whatever the sequences."""
         import torch
-        n = strata_kv4_attention_workspace_bytes(self.desc, n_q_heads)
+        n = strata_kv4_attention_workspace_bytes(self.desc, _int32(n_q_heads, "n_q_heads"))
         if n == 0:
             raise ValueError(f"{n_q_heads} query heads over {self.n_kv_heads} KV heads")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -631,7 +640,8 @@ class Kv4Cache:
                 workspace = self.attention_workspace(heads)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"the workspace is on {workspace.device}, not contiguous on GPU {dev}")
-        desc = strata_kv4_attn_desc(B, heads, max_q_len, block_table.shape[1], n, qt, ot, window,
+        desc = strata_kv4_attn_desc(B, heads, _int32(max_q_len, "max_q_len"), block_table.shape[1], n, qt, ot,
+                                    _int32(window, "window"),
                                     D ** -0.5 if scale is None else scale)
         _on(dev, _lib.strata_kv4_attention, self._desc, ctypes.addressof(desc), handle, where, q.data_ptr(),
             q_offsets.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), out.data_ptr(), workspace.data_ptr(),

@@ -158,3 +158,21 @@ def test_closed_rope_is_refused(rig):
     with pytest.raises(ValueError, match="closed"):
         rope.apply(rig.bf16(3, 8, 128), rig.i32(3))
     assert not rig.calls
+
+
+@pytest.mark.parametrize("wide", [1 << 32, (1 << 32) + 5, (1 << 31), -(1 << 32) + 3])
+def test_numbers_wider_than_the_fields_are_refused(rig, wide):
+    """The library's structures hold 32-bit numbers; ctypes keeps the low bits of a wider one, and a window of 2^32
+    would be no window."""
+    cache = rig.cache()
+    ok = dict(max_q_len=2, window=0)
+    for kw in (dict(window=wide), dict(max_q_len=wide)):
+        with pytest.raises(ValueError):
+            cache.attention(rig.bf16(3, 8, 128), rig.i32(3), rig.i32(2), rig.i32(2, 2), **{**ok, **kw})
+    with pytest.raises(ValueError):
+        cache.attention_workspace(wide + 8)
+    for kw in (dict(head_dim=wide + 128, rotary_dim=64), dict(rotary_dim=wide + 64),
+               dict(scaling="yarn", factor=2.0, original_max_position=wide + 4096)):
+        with pytest.raises((ValueError, rig.S.StrataError)):
+            rig.S.Rope(**{"head_dim": 128, **kw})
+    assert not rig.calls
