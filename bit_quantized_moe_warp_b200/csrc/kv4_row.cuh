@@ -41,10 +41,14 @@ __device__ __forceinline__ uint64_t rope_freq(const RopeTable &t, int i) {
 }
 
 // position * f / (2 pi) modulo one turn: the product wraps modulo 2^64, which
-// is exactly one turn, so a far position loses no bits; as a signed fraction
-// of half turns in [-1, 1).
+// is exactly one turn, so a far position loses no bits. Unsigned, since only
+// there wrapping is defined; read as a signed number it is the fraction of a
+// half turn in [-1, 1).
+__host__ __device__ __forceinline__ uint64_t turn_of(uint64_t freq, int32_t position) {
+    return (uint64_t)(int64_t)position * freq;
+}
 __device__ __forceinline__ double half_turns(const RopeTable &t, int i, int position) {
-    return (double)(int64_t)((uint64_t)(int64_t)position * rope_freq(t, i)) * 0x1p-63;
+    return (double)(int64_t)turn_of(rope_freq(t, i), position) * 0x1p-63;
 }
 
 // (cos, sin) of pair i: fp64, rounded once to fp32 (the bits that
@@ -59,7 +63,7 @@ __device__ __forceinline__ float2 rope_cs(const RopeTable &t, int i, int positio
 // the turn's fraction, then the hardware's sine and cosine (off by 2^-20.9 at
 // most in [-pi, pi]; the row is rounded to fp16, 2^-11, next)
 __device__ __forceinline__ float2 rope_cs_f32(const RopeTable &t, int i, int position) {
-    const int32_t turn = (int32_t)((uint64_t)((int64_t)position * (int64_t)rope_freq(t, i)) >> 32);
+    const int32_t turn = (int32_t)(turn_of(rope_freq(t, i), position) >> 32);
     const float x = (float)turn * 0x1.921fb6p-30f;  // pi 2^-31 a unit
     return make_float2(__cosf(x) * (float)t.m, __sinf(x) * (float)t.m);
 }
