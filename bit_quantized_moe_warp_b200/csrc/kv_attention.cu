@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
         const int last_row = by_group(a, row0 + rows - 1);
         const int full_hi = p_first + by_group(a, row0);
         const int full_lo = a.d.window > 0 ? (int)max((int64_t)p_first + last_row - a.d.window, (int64_t)-1) : -1;
+        // keys that no row sees, (.., any_lo] and [any_hi, ..), may hold anything
+        const int any_lo = a.d.window > 0 ? (int)max((int64_t)full_hi - a.d.window, (int64_t)-1) : -1;
+        const int any_hi = min(p_first + last_row + 1, s.L);
 
         // word t of block 0 of key g; word g / 2 of block 0 of key 2t, and the half of it with values 4g .. 4g + 3
         const uint32_t k_base = code_chunk<D>(g, 0) + 4 * t, v_base = 16 * D + code_chunk<D>(2 * t, 0) + 4 * (g >> 1);
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
             if (!have) continue;
             const uint32_t st = ring_u + stage * C::STAGE;
             const int j0 = it * kTile;
-            const bool full = have == 3 && j0 + kTile - 1 < s.L;
+            const bool full = have == 3 && j0 + kTile - 1 < any_hi && j0 > any_lo;
 
             // V scales in key pairs, [2][8 pairs][NB] half2
             float2 e[2][2];
@@ -454,11 +457,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32, (Split<D, NT>::CTAS_PER_SM))
                         const uint32_t at = st + 34 * D + h * D + (2 * g * NB + ((t + 4 * i) & (NB - 1))) * 2;
                         x[h][i] = lds_half(at) | lds_half(at + 2 * NB) << 16;
                     }
-                if (!full) {  // whatever lies behind the sequence or was never copied
+                if (!full) {  // whatever no row sees or was never copied
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int j = j0 + 16 * h + 2 * g;
-                        const uint32_t keep = have >> h & 1 ? (j < s.L ? 0xffffu : 0u) | (j < s.L - 1 ? 0xffff0000u : 0u) : 0u;
+                        const uint32_t keep = have >> h & 1 ? (j < any_hi && j > any_lo ? 0xffffu : 0u) |
+                                                                  (j + 1 < any_hi && j >= any_lo ? 0xffff0000u : 0u)
+                                                            : 0u;
 #pragma unroll
                         for (int i = 0; i < N; ++i) x[h][i] &= keep;
                     }

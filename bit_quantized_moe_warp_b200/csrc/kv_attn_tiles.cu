@@ -527,10 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *table = a.table + (int64_t)p.b * a.d.max_pages;
             const uint8_t *codes = static_cast<const uint8_t *>(is_v ? a.c.v_codes : a.c.k_codes) + part * (C::NW * 16);
             const uint8_t *vsc = static_cast<const uint8_t *>(a.c.v_scales), *ksc = static_cast<const uint8_t *>(a.c.k_scales);
+            // what no row of the item sees is not read: it may hold anything
+            const int pos0 = p.s.L - p.s.n, any_hi = min(pos0 + by_group(a, p.it.row0 + p.it.rows - 1) + 1, p.s.L);
+            const int any_lo = a.d.window > 0 ? (int)max((int64_t)pos0 + by_group(a, p.it.row0) - a.d.window, (int64_t)-1) : -1;
             uint32_t page = ~0u;
             auto find = [&](int jj) {  // the page of this thread's key in tile jj
                 const int64_t key = (int64_t)(p.kt0 + jj) * TK + row;
-                page = jj < p.nt && key < p.s.L ? (uint32_t)__ldg(table + (key >> a.page_shift)) : ~0u;
+                page = jj < p.nt && key < any_hi && key > any_lo ? (uint32_t)__ldg(table + (key >> a.page_shift)) : ~0u;
             };
             uint4 w[C::NW];
             uint32_t vs[NB / 2], ks[NB / 2];

@@ -138,7 +138,10 @@ strata_status strata_kv4_copy_pages(const strata_kv4_cache *caches, int32_t n_ca
  * head h reads KV head h / (n_q_heads / n_kv_heads).
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j,  bf16.
  * A query that sees no key gives zeros. Positions on a page that is negative
- * or >= n_pages (an evicted page) count as masked. Lengths are clamped to
+ * or >= n_pages (an evicted page) count as masked. Slots that no query of a
+ * sequence sees (in front of its first query's window, behind its last token)
+ * may hold anything, NaN scales too; the scales of the others must be finite,
+ * as the codec leaves them. Lengths are clamped to
  * 0 <= L <= max_pages * page_size and the offsets to 0..n_tokens; query rows
  * outside every sequence, in front of, between or behind them, are not read
  * and their rows of out are left as they were.

@@ -41,3 +41,22 @@ def test_stream_without_buffers(q_len, raw):
         assert same_bits(got, want)
         assert same_bits(rows, turned)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 5, 70])
+@pytest.mark.parametrize("window", [1, 21, 150])
+def test_garbage_in_front_of_the_window(D, q_len, window):
+    """Positions in front of the first query's window may hold anything: not-a-number and infinite scales on the page
+    and in the tile where the window begins never count."""
+    c = Case([(q_len, 333), (q_len, 100 + q_len), (q_len, 512)], 8, 2, D, 16, window=window, seed=D + window)
+    live = torch.zeros((c.cache.n_pages, c.page), dtype=torch.bool, device=torch_dev())
+    for b, L in enumerate(c.lens.tolist()):
+        for j in range(max(L - q_len - window + 1, 0), L):
+            live[int(c.table[b, j // c.page]), j % c.page] = True
+    assert not bool(live.all())
+    for i, poison in ((1, float("nan")), (3, float("inf"))):
+        t = c.cache.tensors[i]
+        t.copy_(torch.where(live[:, None, :, None], t, torch.full_like(t, poison)))
+    c.cache.tensors[3][..., 0].masked_fill_(~live[:, None], float("nan"))
+    c.check()
