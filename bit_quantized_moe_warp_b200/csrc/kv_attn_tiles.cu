@@ -817,6 +817,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w[e] = ex2(z.x), w[e + 1] = ex2(z.y);
                     }
                 };
+                // The same with x fg rounded first, as it was for the maximum: of logits from
+                // 2^27 on, fp32 numbers lie so far apart that the unrounded product can pass
+                // M by more than fp16 holds, or stay behind it by as much.
+                auto weigh_rounded = [&](const float (&x)[32], float (&w)[32], float fg) {
+                    const uint64_t f2 = pack2(fg, fg), m2 = pack2(-M, -M);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 z = unpack2(add2(fma2(pack2(x[e], x[e + 1]), f2, 0), m2));
+                        w[e] = ex2(z.x), w[e + 1] = ex2(z.y);
+                    }
+                };
                 auto pack = [&](const float (&w)[32], uint32_t (&y)[16]) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) y[e] = h2_bits(__floats2half2_rn(w[2 * e], w[2 * e + 1]));
@@ -845,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld32(scol + 32 * g, w);
                             tmem_ld_wait();  // ends the load ahead too
                             move(largest(w) * fac, g);
-                            weigh(w, w, fac);
+                            weigh_rounded(w, w, fac);
                             pack(w, y);
                         }
                         tmem_st16(scol + 16 * g, y);  // columns that were read before
@@ -873,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float top = largest(x) * fg;
                         if (__any_sync(kFullMask, top > M + 11.f)) move(top, g);
                         uint32_t y[16];
-                        weigh(x, x, fg);
+                        weigh_rounded(x, x, fg);
                         pack(x, y);
                         tmem_st16(scol + 16 * g, y);
                         if (own) {

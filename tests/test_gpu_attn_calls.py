@@ -3,6 +3,7 @@ that test_gpu_attn.py does not make; its cases and bounds are used here."""
 import pytest
 import torch
 
+import attn_ref as R
 from gpu_harness import torch_dev
 from test_gpu_attn import Case
 
@@ -60,3 +61,36 @@ def test_garbage_in_front_of_the_window(D, q_len, window):
         t.copy_(torch.where(live[:, None, :, None], t, torch.full_like(t, poison)))
     c.cache.tensors[3][..., 0].masked_fill_(~live[:, None], float("nan"))
     c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 6, 70])
+@pytest.mark.parametrize("gain", [2.0**6, 2.0**12, 2.0**20, 2.0**30, 1.7e9, 7.3e7, -(2.0**12), -(2.0**30), -3.3e8])
+@pytest.mark.parametrize("place", [3, 150])
+def test_logits_of_a_great_size(D, q_len, gain, place):
+    """Logits so large that fp32 numbers of their size lie 8 and more apart, with one key far above the others: the
+    result is that key's value.
+
+    Every key is a multiple s of one row, and the queries are `gain` times that row, so the logits are gain * s times a
+    positive number. The winner's logit is ahead by at least half its size or by its size, thousands at least, so all
+    other weights are 0. Its own weight and value are rounded to fp16 (2^-11 each, the weight times the value's scale
+    once more), the sums add 2^-18, the result is rounded to bf16 (2^-8)."""
+    dev = torch_dev()
+    c = Case([(q_len, 333), (q_len, 160 + q_len)], 8, 2, D, 16, seed=D + q_len)
+    kc, ks = c.cache.tensors[:2]
+    g = torch.Generator(device=dev).manual_seed(D)
+    row = torch.randint(1, 16, (D,), generator=g, device=dev)  # codes; the row they stand for is row - 8
+    kc.copy_((row[0::2] | row[1::2] << 4).to(torch.uint8).expand_as(kc))
+    ks.fill_(2.0**12 if gain > 0 else 0.5)
+    for b in range(2):
+        page = int(c.table[b, place // c.page])
+        ks[page, :, place % c.page] = 2.0**13 if gain > 0 else 0.125
+    c.q.copy_((gain * (row.double() - 8) @ R.sylvester(D, dev)).to(torch.bfloat16).expand_as(c.q))
+    c.q64 = c.q.double()
+    out = c.run().double()
+    want = torch.zeros_like(c.q64)
+    R.attention(c.q64, c.offsets, c.lens, c.table, c.cache.tensors, 0, c.scale, want)
+    assert bool(torch.isfinite(out).all())
+    off, size = (out - want).norm(dim=-1), want.norm(dim=-1)
+    assert bool((size > 0).all())
+    assert float((off / size).max()) <= 2.0**-8 + 3 * 2.0**-11 + 2.0**-18
