@@ -737,7 +737,8 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
                                 cache->n_kv_heads);
     if (d->n_seqs < 0 || d->n_tokens < 0 || d->max_q_len < 0 || d->max_pages < 0 || d->window < 0)
         return strata_set_error(STRATA_ERR_INVALID_ARG, "a negative count in the desc");
-    if (!std::isfinite(d->scale)) return strata_set_error(STRATA_ERR_INVALID_ARG, "scale is not finite");
+    const float scale_log2 = d->scale * 1.44269504088896340736f;
+    if (!std::isfinite(scale_log2)) return strata_set_error(STRATA_ERR_INVALID_ARG, "scale log2(e) is not finite in fp32");
     if ((int64_t)d->max_pages * cache->page_size > 0x7fffffff || d->n_tokens > 0x7fffffff)
         return strata_set_error(STRATA_ERR_INVALID_ARG, "2^31 positions or query rows");
     if (rope && rope->desc.head_dim != cache->head_dim)
@@ -765,7 +766,7 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
                static_cast<__nv_bfloat16 *>(out), workspace, d->n_q_heads / cache->n_kv_heads, 0, 0.f, 0};
     while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
     a.group_inv = a.group > 1 ? ~0ull / (uint64_t)a.group + 1 : 0;
-    a.scale_log2 = d->scale * 1.44269504088896340736f;
+    a.scale_log2 = scale_log2;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool two = (int64_t)d->max_q_len * a.group > 8;
     cudaError_t e;

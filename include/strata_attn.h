@@ -151,8 +151,9 @@ strata_status strata_kv4_copy_pages(const strata_kv4_cache *caches, int32_t n_ca
  * q, the probabilities (times the values' scales, or beside scaled values) and,
  * with more than 48 rows max_q_len * n_q_heads / n_kv_heads, the scaled keys
  * enter the tensor cores in fp16 (with power-of-two scales, so that no
- * magnitude of the inputs overflows); the queries' cosines and sines are those
- * of the hardware (2^-20.9). Results do not depend on timing: the same call
+ * magnitude of the inputs overflows fp16; rotated q and logits times log2(e)
+ * have to stay within fp32); the queries' cosines and sines are those of the
+ * hardware (2^-20.9). Results do not depend on timing: the same call
  * gives the same bits, another max_q_len may give others.
  * Any n_seqs and lengths >= 0; q and out 16-byte aligned, token strides
  * multiples of 8, heads head_dim apart.
@@ -168,7 +169,7 @@ typedef struct {
     int64_t q_token_stride;   /* elements */
     int64_t out_token_stride; /* elements */
     int32_t window;           /* 0: every earlier position */
-    float scale;              /* finite */
+    float scale;              /* finite, scale log2(e) too */
 } strata_kv4_attn_desc;
 
 /* Workspace of strata_kv4_attention on this cache's shape for n_q_heads query

@@ -176,3 +176,19 @@ def test_numbers_wider_than_the_fields_are_refused(rig, wide):
         with pytest.raises((ValueError, rig.S.StrataError)):
             rig.S.Rope(**{"head_dim": 128, **kw})
     assert not rig.calls
+
+
+def test_scale_beyond_fp32_is_refused(rig):
+    """The kernels work with scale * log2(e) in fp32: a scale that overflows there would make every row NaN."""
+    S = rig.S
+    c = S.strata_kv4_cache(0x10000, 0x20000, 0x30000, 0x40000, 10, 2, 16, 128)
+    real = ctypes.CDLL(S.LIB_PATH).strata_kv4_attention
+    real.restype, real.argtypes = S._SIGS["strata_kv4_attention"]
+
+    def status(scale):  # of a call without tokens, which has nothing to do
+        d = S.strata_kv4_attn_desc(0, 4, 1, 3, 0, 512, 512, 0, scale)
+        return real(ctypes.addressof(c), ctypes.addressof(d), *[None] * 8, 0, None)
+
+    assert status(2.3e38) == status(-2.3e38) == S.STRATA_OK
+    for scale in (2.4e38, 3.4e38, -2.4e38):
+        assert status(scale) == S.STRATA_ERR_INVALID_ARG
