@@ -529,7 +529,7 @@ class Rope:
             pass
 
     def apply(self, x, positions, out=None, stream=None):
-        """x [tokens, heads, head_dim] bf16 (any token and head strides), positions int32 [tokens]; out may be x.
+        """x [tokens, heads, head_dim] bf16 (token by token or head by head), positions int32 [tokens]; out may be x.
         An `out` that the call makes belongs to `stream`, like any tensor made under torch.cuda.stream."""
         import torch
         if self.handle is None:

@@ -152,6 +152,13 @@ __global__ void __launch_bounds__(kThreads) k_rope_scalar(const __grid_constant_
     }
 }
 
+// rows one behind the other, token by token or head by head
+bool rows_apart(int64_t tok, int64_t head, int64_t tokens, int64_t heads, int D) {
+    auto holds = [&](int64_t inner, int64_t n_inner, int64_t outer, int64_t n_outer) {
+        return (n_inner == 1 || inner >= D) && (n_outer == 1 || outer >= (__int128)(n_inner - 1) * inner + D);
+    };
+    return holds(head, heads, tok, tokens) || holds(tok, tokens, head, heads);
+}
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
@@ -237,11 +244,10 @@ extern "C" strata_status strata_rope_apply(strata_rope rope, const void *x, int6
     if ((x_token_stride | x_head_stride | out_token_stride | out_head_stride) & 7)
         return strata_set_error(STRATA_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
     const int D = rope->desc.head_dim;
-    if (n_heads > 1 && (x_head_stride < D || out_head_stride < D))
-        return strata_set_error(STRATA_ERR_INVALID_ARG, "head strides must be at least head_dim");
-    const int64_t need_x = (n_heads - 1) * x_head_stride + D, need_o = (n_heads - 1) * out_head_stride + D;
-    if (n_tokens > 1 && (x_token_stride < need_x || out_token_stride < need_o))
-        return strata_set_error(STRATA_ERR_INVALID_ARG, "token strides must hold the heads of a token");
+    if (!rows_apart(x_token_stride, x_head_stride, n_tokens, n_heads, D) ||
+        !rows_apart(out_token_stride, out_head_stride, n_tokens, n_heads, D))
+        return strata_set_error(STRATA_ERR_INVALID_ARG,
+                                "strides must keep rows of head_dim values apart, token by token or head by head");
     if (n_heads > (1 << 20)) return strata_set_error(STRATA_ERR_INVALID_ARG, "n_heads %d", n_heads);
     RopeArgs a{static_cast<const __nv_bfloat16 *>(x), static_cast<__nv_bfloat16 *>(out), positions,
                x_token_stride, x_head_stride, out_token_stride, out_head_stride, n_tokens, n_heads, D, 1, 0, 0, 0};

@@ -79,7 +79,8 @@ strata_status strata_rope_destroy(strata_rope rope);
  * Row (t, h) of x starts at x + t * x_token_stride + h * x_head_stride
  * (elements), likewise out. out may be x with the same strides (in place);
  * any other overlap is not allowed. x and out 16-byte aligned, strides
- * multiples of 8 and head strides >= head_dim, positions int32 [n_tokens].
+ * multiples of 8 that keep the rows apart: token strides that hold a token's
+ * heads, or head strides that hold a head's tokens; positions int32 [n_tokens].
  * n_tokens or n_heads 0: no-op. Errors: INVALID_ARG, CUDA. */
 strata_status strata_rope_apply(strata_rope rope, const void *x, int64_t x_token_stride, int64_t x_head_stride,
                                 const int32_t *positions, int64_t n_tokens, int32_t n_heads, void *out,

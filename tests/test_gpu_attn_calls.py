@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import attn_ref as R
-from gpu_harness import torch_dev
+from gpu_harness import S, torch_dev
 from test_gpu_attn import Case
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,24 @@ def test_logits_of_a_great_size(D, q_len, gain, place):
     off, size = (out - want).norm(dim=-1), want.norm(dim=-1)
     assert bool((size > 0).all())
     assert float((off / size).max()) <= 2.0**-8 + 3 * 2.0**-11 + 2.0**-18
+
+
+@pytest.mark.parametrize("layout,rd", [("half", 128), ("interleaved", 64), ("half", 20)])
+@pytest.mark.parametrize("n,heads", [(1, 5), (37, 5), (300, 3), (9, 1)])
+def test_rotary_of_rows_head_by_head(layout, rd, n, heads):
+    """Rows of a head together, as a transposed view has them, on either side and in place."""
+    dev = torch_dev()
+    rope = S().Rope(128, rd, layout=layout)
+    g = torch.Generator(device=dev).manual_seed(n)
+    x = torch.randn((n, heads, 128), generator=g, device=dev).to(torch.bfloat16)
+    pos = torch.arange(n, dtype=torch.int32, device=dev) * 91
+    want = rope.apply(x, pos)
+    by_head = x.transpose(0, 1).contiguous().transpose(0, 1)
+    assert n == 1 or heads == 1 or by_head.stride()[:2] == (128, n * 128)
+    assert same_bits(rope.apply(by_head, pos), want)
+    out = torch.zeros((heads, n, 128), dtype=torch.bfloat16, device=dev).transpose(0, 1)
+    assert same_bits(rope.apply(x, pos, out), want)
+    assert same_bits(rope.apply(by_head, pos, by_head), want)
+    if n > 1 and heads > 1:
+        with pytest.raises(S().StrataError):  # every token in one place
+            rope.apply(x, pos, x[:1].expand(n, -1, -1))
