@@ -122,6 +122,7 @@ _SIGS = {
     "strata_kv4_copy_pages": (I32, [V, I32, V, V, I64, V]),
     "strata_kv4_attention_workspace_bytes": (SZ, [V, I32]),
     "strata_kv4_attention": (I32, [V, V, V, V, V, V, V, V, V, V, SZ, V]),
+    "strata_selftest_attention_timeout": (I32, [V, V, V, V, V, V, V, V, SZ, I32, I32, I32, V]),
     "strata_status_string": (ctypes.c_char_p, [I32]),
     "strata_last_error": (ctypes.c_char_p, []),
 }
@@ -335,6 +336,14 @@ def strata_kv4_attention(cache, desc, rope, positions, q, q_offsets, kv_lens, bl
     _check(_lib.strata_kv4_attention(ctypes.addressof(cache), ctypes.addressof(desc), rope, _ptr(positions), _ptr(q),
                                      _ptr(q_offsets), _ptr(kv_lens), _ptr(block_table), _ptr(out), _ptr(workspace),
                                      workspace_bytes, _stream(stream)))
+
+
+def strata_selftest_attention_timeout(cache, desc, q, q_offsets, kv_lens, block_table, out, workspace, workspace_bytes,
+                                      role, every, piece, stream=None):
+    _check(_lib.strata_selftest_attention_timeout(ctypes.addressof(cache), ctypes.addressof(desc), _ptr(q),
+                                                  _ptr(q_offsets), _ptr(kv_lens), _ptr(block_table), _ptr(out),
+                                                  _ptr(workspace), workspace_bytes, role, every, piece,
+                                                  _stream(stream)))
 
 
 def strata_rmsnorm_bf16(x, out, n_tokens, d, eps, stream=None):

@@ -724,11 +724,10 @@ extern "C" size_t strata_kv4_attention_workspace_bytes(const strata_kv4_cache *c
     return sizeof(Span) * kSplitMaxCtas + (split > tiles ? split : tiles);
 }
 
-extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, const strata_kv4_attn_desc *d,
-                                              strata_rope rope, const int32_t *positions, const void *q,
-                                              const int32_t *q_offsets, const int32_t *kv_lens,
-                                              const int32_t *block_table, void *out, void *workspace,
-                                              size_t workspace_bytes, strata_stream_t stream) {
+static strata_status attention(const strata_kv4_cache *cache, const strata_kv4_attn_desc *d, strata_rope rope,
+                               const int32_t *positions, const void *q, const int32_t *q_offsets,
+                               const int32_t *kv_lens, const int32_t *block_table, void *out, void *workspace,
+                               size_t workspace_bytes, const AttnStall *stall, strata_stream_t stream) {
     const strata_status s = strata_check_kv4_cache(cache);
     if (s != STRATA_OK) return s;
     if (!d) return strata_set_error(STRATA_ERR_INVALID_ARG, "NULL desc");
@@ -770,7 +769,9 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool two = (int64_t)d->max_q_len * a.group > 8;
     cudaError_t e;
-    if ((int64_t)d->max_q_len * a.group > kSplitMostRows)
+    if (stall)
+        e = launch_attn_tiles_stalled(tab, a, *stall, st);
+    else if ((int64_t)d->max_q_len * a.group > kSplitMostRows)
         e = launch_attn_tiles(tab, a, st);
     else if (cache->head_dim == 64)
         e = two ? launch_split<64, 2>(tab, a, st) : launch_split<64, 1>(tab, a, st);
@@ -780,4 +781,26 @@ extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, con
         e = launch_split<256, 1>(tab, a, st);
     if (e != cudaSuccess) return strata_set_error(STRATA_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return STRATA_OK;
+}
+
+extern "C" strata_status strata_kv4_attention(const strata_kv4_cache *cache, const strata_kv4_attn_desc *d,
+                                              strata_rope rope, const int32_t *positions, const void *q,
+                                              const int32_t *q_offsets, const int32_t *kv_lens,
+                                              const int32_t *block_table, void *out, void *workspace,
+                                              size_t workspace_bytes, strata_stream_t stream) {
+    return attention(cache, d, rope, positions, q, q_offsets, kv_lens, block_table, out, workspace, workspace_bytes,
+                     nullptr, stream);
+}
+
+extern "C" strata_status strata_selftest_attention_timeout(const strata_kv4_cache *cache, const strata_kv4_attn_desc *d,
+                                                           const void *q, const int32_t *q_offsets,
+                                                           const int32_t *kv_lens, const int32_t *block_table,
+                                                           void *out, void *workspace, size_t workspace_bytes,
+                                                           int32_t role, int32_t every, int32_t piece,
+                                                           strata_stream_t stream) {
+    if (role < 0 || role > 3 || every < 1 || piece < 0)
+        return strata_set_error(STRATA_ERR_INVALID_ARG, "role %d, every %d, piece %d", role, every, piece);
+    const AttnStall stall{role, every, piece};
+    return attention(cache, d, nullptr, nullptr, q, q_offsets, kv_lens, block_table, out, workspace, workspace_bytes,
+                     &stall, stream);
 }

@@ -267,8 +267,15 @@ cudaError_t launch_join(const AttnArgs &a, int ctas, cudaStream_t st) {
         return launch_early(k_attn_join<D, ROWS>, dim3(ctas, y), 512, 0, st, a);
 }
 
-// Many query rows (kv_attn_tiles.cu): bytes of its partial results, and the launch
+// Many query rows (kv_attn_tiles.cu): bytes of its partial results, the launch, and
+// the launch of the self test, in which a role of every `every`-th CTA stops
+// arriving from its piece `piece` on
+struct AttnStall {
+    int role;  // 0 keys, 1 values, 2 weights, 3 query rows
+    int every, piece;
+};
 size_t attn_tiles_part_bytes(int head_dim);
 cudaError_t launch_attn_tiles(const RopeTable &tab, const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_tiles_stalled(const RopeTable &tab, const AttnArgs &a, const AttnStall &stall, cudaStream_t st);
 
 }  // namespace strata

@@ -133,23 +133,24 @@ STRATA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" :
 // follows (.aligned instructions, uniform registers) needs the warp in one piece,
 // which lanes that leave a loop one by one do not promise.
 template <typename Test>
-STRATA_DEV bool warp_poll(Test &&test, volatile int *abort) {
+STRATA_DEV bool warp_poll(Test &&test, volatile int *abort, uint64_t limit_ns) {
     if (__all_sync(kFullMask, test())) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t i = 1;; ++i) {
         if (__all_sync(kFullMask, test())) return true;
-        if ((i & 63u) == 0 && __any_sync(kFullMask, (abort && *abort) || globaltimer() - t0 > kWaitLimitNs)) {
+        if ((i & 63u) == 0 && __any_sync(kFullMask, (abort && *abort) || globaltimer() - t0 > limit_ns)) {
             if (abort) *abort = 1;
             return false;
         }
     }
 }
-STRATA_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return warp_poll([&]() { return mbar_try_wait(bar, parity); }, abort);
+template <uint64_t LIMIT>
+STRATA_DEV bool warp_wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return warp_poll([&]() { return mbar_try_wait(bar, parity); }, abort, LIMIT);
 }
 // until a number in shared memory has come up to `least`
-STRATA_DEV bool count_wait(volatile uint32_t *count, uint32_t least, volatile int *abort) {
-    const bool ok = warp_poll([&]() { return *count >= least; }, abort);
+STRATA_DEV bool count_wait(volatile uint32_t *count, uint32_t least, volatile int *abort, uint64_t limit_ns) {
+    const bool ok = warp_poll([&]() { return *count >= least; }, abort, limit_ns);
     __threadfence_block();
     return ok;
 }
@@ -265,10 +266,23 @@ STRATA_DEV int64_t head_units(const AttnArgs &a, const SeqBase &s, int lane) {
     return v;
 }
 
-template <int D>
+// STALL: the self test of waits that run out, with a limit of its own. Where one
+// does, everybody else in the CTA gives up soon after, and the softmax warps make
+// every row that this CTA still owes NaN: those of the piece at hand, and without
+// another wait those of the pieces behind it. A row that a broken CTA has a part
+// of cannot pass for a result.
+template <int D, bool STALL>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_tiles(const __grid_constant__ RopeTable tab, const __grid_constant__ AttnArgs a) {
+    k_attn_tiles(const __grid_constant__ RopeTable tab, const __grid_constant__ AttnArgs a,
+                 const __grid_constant__ AttnStall stall) {
     using C = Tiles<D>;
+    constexpr uint64_t kLimitNs = STALL ? 5000000ull : kWaitLimitNs;
+    auto warp_wait = [](uint64_t *bar, uint32_t parity, volatile int *abort) {
+        return warp_wait_for<kLimitNs>(bar, parity, abort);
+    };
+    auto arrives = [&](int role, uint32_t piece) {
+        return !STALL || role != stall.role || blockIdx.x % stall.every != 0 || piece < (uint32_t)stall.piece;
+    };
     constexpr int NB = C::NB, TK = C::TK, P = D / 32, SLOTS = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -514,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!pairs || i) umma_done(&vempty[c & 1], me);
                 if (n + 2 < steps) ok = product_s(n + 2);
             }
+            if (!ok) __threadfence_block();  // who sees this barrier sees s_abort
             umma_done(&odone, me);
             warp_wait(&odone, p.count & 1, nullptr);  // before anything is torn down
             return ok;
@@ -561,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             find(1);
             // The second O of the last dual piece was added up in the keys' buffers. These
             // warps may be pieces ahead, where a barrier's parity says nothing: a count.
-            if (p.nt > 0 && p.after_dual && !count_wait(&s_begun, p.count + 1, &s_abort)) return false;
+            if (p.nt > 0 && p.after_dual && !count_wait(&s_begun, p.count + 1, &s_abort, kLimitNs)) return false;
             for (int jj = 0; jj < p.nt; ++jj) {
                 const uint32_t c = p.tc + jj;
                 // the scales' ranges decide for 32 keys at a time; keys and values see the same numbers
@@ -631,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                if (lane == 0 && arrives(is_v ? 1 : 0, p.count)) mbar_arrive(full);
             }
             return true;
         });
@@ -715,13 +730,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                // the factors are read by other warps; a wait that ran out ends the work for all of them
-                if (named_barrier_or(2, 256, *(volatile int *)&s_abort != 0)) return false;
+                // the factors are read by other warps; after a wait that ran out all of them only mark their rows
+                if (named_barrier_or(2, 256, *(volatile int *)&s_abort != 0)) {
+                    if (p.whole) {
+                        for (int i = threadIdx.x; i < p.it.rows * (D / 8); i += 256) {
+                            const int row = p.it.row0 + i / (D / 8), tok = by_group(a, row);
+                            const int h = p.hk * a.group + row - tok * a.group;
+                            *reinterpret_cast<uint4 *>(a.out + (p.s.t0 + tok) * a.d.out_token_stride + (int64_t)h * D +
+                                                       i % (D / 8) * 8) =
+                                make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                        }
+                    } else {
+                        float4 *part = reinterpret_cast<float4 *>(parts + (int64_t)(blockIdx.x * 2 + slot_of(p)) * C::ROWS * C::PART);
+                        for (int i = threadIdx.x; i < (D / 4 + 1) * C::ROWS; i += 256) part[i] = make_float4(NAN, NAN, NAN, NAN);
+                    }
+                    return true;
+                }
                 if (threadIdx.x == 0) {
                     __threadfence_block();
                     *(volatile uint32_t *)&s_begun = p.count + 1;
                 }
-                if (lane == 0) mbar_arrive(&qfull);
+                if (lane == 0 && arrives(3, p.count)) mbar_arrive(&qfull);
             }
             const int slot = warp >> 2, tr = threadIdx.x & 127;
             const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
@@ -899,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pready[i]);
+                if (lane == 0 && arrives(2, p.count)) mbar_arrive(&pready[i]);
             }
             // ---- the rows' results
             ok = warp_wait(&odone, p.count & 1, &s_abort) && ok;  // the next piece's rows overwrite these, too
@@ -939,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            float z = mine ? y[e] * f0 : 0.f;
+                            float z = (mine ? y[e] : 0.f) * f0;  // NaN where f0 is
                             if (p.dual && p.nt > 1) z = fmaf(other[(col + e) * 128 + r], f1, z);
                             x[(e & 24) + value_at(e & 7)] = z;
                         }
@@ -1013,13 +1042,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
-cudaError_t launch(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
+template <int D, bool STALL>
+cudaError_t launch(const RopeTable &tab, const AttnArgs &a, const AttnStall &stall, cudaStream_t st) {
     using C = Tiles<D>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(k_attn_tiles<D>, C::SMEM, done);
+    const cudaError_t e = allow_smem(k_attn_tiles<D, STALL>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    const cudaError_t l = launch_early(k_attn_tiles<D>, dim3(kSms), kThreads, C::SMEM, st, tab, a);
+    const cudaError_t l = launch_early(k_attn_tiles<D, STALL>, dim3(kSms), kThreads, C::SMEM, st, tab, a, stall);
     return l != cudaSuccess ? l : launch_join<D, C::ROWS, true>(a, kSms, st);
 }
 
@@ -1030,10 +1059,17 @@ size_t attn_tiles_part_bytes(int head_dim) {
     return 2 * rows * kSms * sizeof(float) * (head_dim + 4);
 }
 
+template <bool STALL>
+static cudaError_t launch_any(const RopeTable &tab, const AttnArgs &a, const AttnStall &stall, cudaStream_t st) {
+    if (a.c.head_dim == 64) return launch<64, STALL>(tab, a, stall, st);
+    if (a.c.head_dim == 128) return launch<128, STALL>(tab, a, stall, st);
+    return launch<256, STALL>(tab, a, stall, st);
+}
 cudaError_t launch_attn_tiles(const RopeTable &tab, const AttnArgs &a, cudaStream_t st) {
-    if (a.c.head_dim == 64) return launch<64>(tab, a, st);
-    if (a.c.head_dim == 128) return launch<128>(tab, a, st);
-    return launch<256>(tab, a, st);
+    return launch_any<false>(tab, a, AttnStall{}, st);
+}
+cudaError_t launch_attn_tiles_stalled(const RopeTable &tab, const AttnArgs &a, const AttnStall &stall, cudaStream_t st) {
+    return launch_any<true>(tab, a, stall, st);
 }
 
 }  // namespace strata

@@ -160,7 +160,8 @@ strata_status strata_kv4_copy_pages(const strata_kv4_cache *caches, int32_t n_ca
  * multiples of 8, heads head_dim apart.
  * workspace: strata_kv4_attention_workspace_bytes() bytes, 16-byte aligned,
  * its contents neither read nor kept between calls; calls that may overlap
- * need one each. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * need one each. Should a wait inside the tensor-core kernel run out (2 s), the
+ * rows concerned become NaN. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 typedef struct {
     int32_t n_seqs;
     int32_t n_q_heads;        /* a multiple of n_kv_heads */
@@ -183,6 +184,18 @@ strata_status strata_kv4_attention(const strata_kv4_cache *cache, const strata_k
                                    const int32_t *positions, const void *q, const int32_t *q_offsets,
                                    const int32_t *kv_lens, const int32_t *block_table, void *out, void *workspace,
                                    size_t workspace_bytes, strata_stream_t stream);
+
+/* Failure-detection self test: the attention by its tensor-core kernel without
+ * rotary, in which one role of every `every`-th thread block stops signalling
+ * from its piece of work number `piece` on (role 0: expanded keys, 1: expanded
+ * values, 2: weights, 3: query rows) and waits give up after 5 ms. A query row
+ * that such a piece, or one behind it, has part in comes out as NaN, every other
+ * as strata_kv4_attention computes it (or NaN, where it was done last before). */
+strata_status strata_selftest_attention_timeout(const strata_kv4_cache *cache, const strata_kv4_attn_desc *desc,
+                                                const void *q, const int32_t *q_offsets, const int32_t *kv_lens,
+                                                const int32_t *block_table, void *out, void *workspace,
+                                                size_t workspace_bytes, int32_t role, int32_t every, int32_t piece,
+                                                strata_stream_t stream);
 
 #ifdef __cplusplus
 }

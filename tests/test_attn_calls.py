@@ -192,3 +192,15 @@ def test_scale_beyond_fp32_is_refused(rig):
     assert status(2.3e38) == status(-2.3e38) == S.STRATA_OK
     for scale in (2.4e38, 3.4e38, -2.4e38):
         assert status(scale) == S.STRATA_ERR_INVALID_ARG
+
+
+def test_timeout_selftest_refusals(rig):
+    S = rig.S
+    c = S.strata_kv4_cache(0x10000, 0x20000, 0x30000, 0x40000, 10, 2, 16, 128)
+    d = S.strata_kv4_attn_desc(0, 4, 1, 3, 0, 512, 512, 0, 1.0)
+    args = (c, d, 0, 0, 0, 0, 0, 0, 0)
+    for bad in ((-1, 1, 0), (4, 1, 0), (0, 0, 0), (0, 1, -1)):
+        with pytest.raises(S.StrataError) as e:
+            S.strata_selftest_attention_timeout(*args, *bad, stream=0)
+        assert e.value.status == S.STRATA_ERR_INVALID_ARG
+    S.strata_selftest_attention_timeout(*args, 0, 1, 0, stream=0)  # no tokens: nothing to do

@@ -115,3 +115,33 @@ def test_rotary_of_rows_head_by_head(layout, rd, n, heads):
     if n > 1 and heads > 1:
         with pytest.raises(S().StrataError):  # every token in one place
             rope.apply(x, pos, x[:1].expand(n, -1, -1))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("role", [0, 1, 2, 3])
+@pytest.mark.parametrize("piece", [0, 1])
+def test_waits_that_run_out_leave_no_row_that_passes_for_a_result(D, role, piece):
+    """Four of the tensor-core kernel's 148 blocks stop signalling (5 ms limit): every row is NaN or what the undisturbed
+    call gives, though result and workspace hold an earlier call's values; and the next call is right again."""
+    lib, dev = S(), torch_dev()
+    # two or three pieces for each block
+    c = Case([(90, 700), (33, 2000)] * 30 + [(60, 60), (7, 3000), (60, 0)], 16, 2, D, 16, seed=D + 8, pad_back=4)
+    ws = c.cache.attention_workspace(16)
+    want = torch.full_like(c.q, 7.5, memory_format=torch.contiguous_format)
+    c.run(want, workspace=ws)
+    n = c.q.shape[0]
+    desc = lib.strata_kv4_attn_desc(len(c.lens), 16, c.max_q, c.table.shape[1], n, c.q.stride(0), 16 * D, 0, c.scale)
+    for fill in (7.5, None):
+        out = want.clone() if fill is None else torch.full_like(want, fill)
+        ws.view(torch.float32).fill_(1.0)  # partial results that look like some
+        lib.strata_selftest_attention_timeout(c.cache.desc, desc, c.q, c.offsets, c.lens, c.table, out, ws, ws.numel(),
+                                              role, 37, piece)
+        torch.cuda.synchronize()
+        lost = out.isnan().all(-1)
+        same = (out.view(torch.int16) == want.view(torch.int16)).all(-1)
+        assert bool((lost | same).all()), f"{int((~(lost | same)).sum())} rows are neither lost nor right"
+        assert bool((out[-4:] == 7.5).all())
+        assert bool(same[:-4].any()) and bool(lost.any())
+    out = torch.full_like(want, 7.5)
+    c.run(out, workspace=ws)
+    assert same_bits(out, want)
