@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import attn_ref as R
+import attn_stat
 from gpu_harness import S, torch_dev
 from test_gpu_attn import Case
 
@@ -145,3 +146,17 @@ def test_waits_that_run_out_leave_no_row_that_passes_for_a_result(D, role, piece
     out = torch.full_like(want, 7.5)
     c.run(out, workspace=ws)
     assert same_bits(out, want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seqs,heads,kv_heads,window", [
+    ([(1, 200_003)], 8, 1, 0), ([(1, 20_000), (1, 77_777), (1, 1025)], 16, 2, 0), ([(2, 131_072)], 8, 1, 0),
+    ([(6, 60_000), (6, 33_333), (6, 1025)], 8, 1, 0), ([(70, 60_001)], 4, 1, 0),
+    ([(300, 20_000), (1, 30_000), (5, 700)], 8, 2, 0), ([(1, 40_000), (200, 30_000)], 8, 2, 9_000)])
+def test_rows_over_long_contexts(D, seqs, heads, kv_heads, window):
+    """Every row within what rounding does in the mean (attn_stat): a lost tile, part or page of any length would show."""
+    c = Case(seqs, heads, kv_heads, D, 64, window=window, rope=(D, "half", "none", 1.0), seed=D + len(seqs))
+    want, limit, inside = attn_stat.attention(c.q64, c.offsets, c.lens, c.table, c.cache.tensors, c.window, c.scale)
+    off = (c.run().double() - want).norm(dim=-1)
+    assert bool(inside.all())
+    assert bool((off <= limit).all()), f"worst {float((off / limit).max()):.3g} of the limit"
