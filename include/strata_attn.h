@@ -110,8 +110,8 @@ typedef struct {
  * one another: rows of two tokens in one slot get mixed. Codes and scales are
  * bit for bit those of strata_rope_apply followed by strata_kv4_encode.
  * Rows (t, h) of k start at k + t * k_token_stride + h * head_dim (elements),
- * likewise v; k and v 16-byte aligned, strides multiples of 8. positions may
- * be NULL when rope is. Inputs must be finite, as for strata_kv4_encode.
+ * likewise v; k and v 16-byte aligned, strides multiples of 8 that hold a
+ * token's heads. positions may be NULL when rope is. Inputs must be finite, as for strata_kv4_encode.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size), CUDA. */
 strata_status strata_kv4_append(const strata_kv4_cache *cache, strata_rope rope, const void *k,
                                 int64_t k_token_stride, const void *v, int64_t v_token_stride,
@@ -157,7 +157,8 @@ strata_status strata_kv4_copy_pages(const strata_kv4_cache *caches, int32_t n_ca
  * hardware (2^-20.9). Results do not depend on timing: the same call
  * gives the same bits, another max_q_len may give others.
  * Any n_seqs and lengths >= 0; q and out 16-byte aligned, token strides
- * multiples of 8, heads head_dim apart.
+ * multiples of 8 that hold a token's heads, heads head_dim apart. out may be q
+ * with the same stride (in place); any other overlap is not allowed.
  * workspace: strata_kv4_attention_workspace_bytes() bytes, 16-byte aligned,
  * its contents neither read nor kept between calls; calls that may overlap
  * need one each. Should a wait inside the tensor-core kernel run out (2 s), the

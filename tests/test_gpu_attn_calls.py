@@ -160,3 +160,82 @@ def test_rows_over_long_contexts(D, seqs, heads, kv_heads, window):
     off = (c.run().double() - want).norm(dim=-1)
     assert bool(inside.all())
     assert bool((off <= limit).all()), f"worst {float((off / limit).max()):.3g} of the limit"
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 6, 120])
+def test_result_in_the_queries_place(D, q_len):
+    """out may be q: every query row is read before its result is written, by whichever block."""
+    c = Case([(q_len, 900), (q_len, 9000), (2, 40)], 16, 2, D, 32, rope=(D, "half", "none", 1.0), seed=q_len + D)
+    want = c.run()
+    wide = torch.full((c.q.shape[0], 19, D), 7.5, dtype=torch.bfloat16, device=torch_dev())
+    for _ in range(5):
+        x = wide[:, 1:17]
+        x.copy_(c.q)
+        c.cache.attention(x, c.offsets, c.lens, c.table, x, max_q_len=c.max_q, scale=c.scale, rope=c.rope,
+                          positions=c.positions)
+        assert same_bits(x, want)
+        assert bool((wide[:, 0] == 7.5).all()) and bool((wide[:, 17:] == 7.5).all())
+
+
+@pytest.mark.parametrize("q_len", [1, 70])
+def test_captured_step(q_len):
+    """A layer's whole step in one graph (a fork's page copy, rotary rows, append, attention, with buffers of the
+    graph's own), replayed on new inputs: the same bits as the calls one by one."""
+    lib, dev = S(), torch_dev()
+    D, heads, hk, page, pages = 128, 16, 2, 16, 80
+    rope = lib.Rope(D, D, layout="half")
+    g = torch.Generator(device=dev).manual_seed(q_len)
+    start = [torch.randint(0, 256, t.shape, generator=g, device=dev, dtype=torch.uint8) if t.dtype == torch.uint8 else
+             torch.rand(t.shape, generator=g, device=dev).half() for t in lib.Kv4Cache.empty(pages, page, hk, D).tensors]
+    lens = torch.tensor([200, 333], dtype=torch.int32, device=dev) + q_len
+    table = torch.arange(2 * 36, dtype=torch.int32, device=dev).view(2, 36)
+    offs = torch.tensor([0, q_len, 2 * q_len], dtype=torch.int32, device=dev)
+
+    def inputs(seed):
+        r = torch.Generator(device=dev).manual_seed(seed)
+        qkv = torch.randn((2 * q_len, heads + 2 * hk, D), generator=r, device=dev).to(torch.bfloat16)
+        pos = torch.cat([torch.arange(int(n) - q_len, int(n), device=dev) for n in lens])
+        slots = torch.cat([table[b].long()[pos[b * q_len : (b + 1) * q_len] // page] * page +
+                           pos[b * q_len : (b + 1) * q_len] % page for b in range(2)])
+        return qkv, pos.to(torch.int32) + seed, slots
+
+    def step(cache, qkv, pos, slots):
+        q, k, v = qkv[:, :heads], qkv[:, heads : heads + hk], qkv[:, heads + hk :]
+        lib.Kv4CacheSet([cache]).copy_pages([3, 5], [75, 76])
+        cache.append(k, v, slots, rope=rope, positions=pos)
+        return rope.apply(k, pos), cache.attention(q, offs, lens, table, max_q_len=q_len, rope=rope, positions=pos)
+
+    def fresh():
+        return lib.Kv4Cache(*(t.clone() for t in start))
+
+    static = [t.clone() for t in inputs(1)]
+    cache = fresh()
+    graph = torch.cuda.CUDAGraph()
+    step(fresh(), *static)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(cache, *static)
+    for seed in (2, 3, 2):
+        other = fresh()
+        for a, b in zip(cache.tensors, start):
+            a.copy_(b)
+        for a, b in zip(static, inputs(seed)):
+            a.copy_(b)
+        graph.replay()
+        want = step(other, *inputs(seed))
+        torch.cuda.synchronize()
+        assert same_bits(got[0], want[0]) and same_bits(got[1], want[1])
+        for a, b in zip(cache.tensors, other.tensors):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("q_len", [1, 70])
+def test_a_page_in_many_tables_and_twice_in_one(q_len):
+    """Sequences that share their prefix's pages, the same page several times in a table, and two views of a cache."""
+    c = Case([(q_len, 500), (q_len, 500), (q_len, 130)], 8, 2, 128, 16, seed=5)
+    c.table[1, :20] = c.table[0, :20]
+    c.table[2] = c.table[0, 1]
+    c.check()
+    c.cache = S().Kv4Cache(*(t.view(t.shape) for t in c.cache.tensors))
+    c.check()
