@@ -17,9 +17,9 @@ namespace {
 
 // ---------------------------------------------------------------- few rows
 // k_attn_split: up to 8 NT query rows of a KV head (tokens x heads of the
-// group) against a long cache, which is read once. Bound by HBM, and close
-// behind by instruction issue: 18 D bytes and about 280 warp instructions a
-// 16-key tile, so everything around the matrix instructions is counted.
+// group) against a long cache, which is read once. Floor: HBM, 36 D bytes a
+// 32-key tile; a tile takes about 740 warp instructions, so everything around
+// the matrix instructions is counted.
 //
 //   * S^T = K Q^T: keys are the 16 rows of m16n8k16, 8 query rows its columns.
 //     A code's nibble under the exponent of 1024 (or, at bits 4..7, of 64) is
@@ -46,18 +46,29 @@ namespace {
 // 131,072 cached tokens of 4 KV heads of 128 30.8 us (2.4 TB/s of the cache's
 // 75.5 MB), 64 sequences of 1,024 to 16,384 69 us (3.3 TB/s), 1 at 777 11 us.
 // About 10 us of each are fixed: three dependent loads (lengths, page table,
-// tile) before the first product, the join of the warps and of the CTAs. In the
-// stream itself 16 warps issue 2.4 to 3 of 4 instructions a cycle and SM, some
-// 740 for 32 keys (245 of them unpacking and adding up values).
+// tile) before the first product, the join of the warps and of the CTAs. Over
+// the whole kernel ncu shows 2.3 of 4 instructions issued a cycle and SM with 16
+// warps on it: neither issue nor HBM (2.8 TB/s) is full, the rest is latency. Of
+// the 740 instructions for 32 keys 245 unpack and add up values.
 // 12 warps instead of 8 for 16 rows: no faster (51 and 54 us, 32 rows, 100,000
 // keys); 2 blocks of 128 registers for 16 rows of 64 values: the same.
 constexpr int kSplitParts = 2 * 16 * kSms;  // rows of partial results: 2 x 8 rows x 296 CTAs or 2 x 16 x 148
 constexpr int kSplitWarps = 8;
 // Rows of a KV head and sequence up to which k_attn_split is launched, 16 at a
-// time, and above which k_attn_tiles. us with one and the other, 8 sequences up
-// to 32,768 / 4 up to 2,000 / 1 of 100,000 keys, 4 KV heads of 128: 32 rows 52,
-// 19, 51 and 67, 25, 72; 48 rows 59, 20, 70 and 65, 28, 75; 64 rows 133, 20, 87
-// and 157, 28, 76. Both take any number.
+// time (8 for head_dim 256), and above which k_attn_tiles. us with one and the
+// other, 4 KV heads:
+//   rows                     8 of 2,048 to 32,768   4 of 500 to 2,000   1 of 100,000
+//   head_dim 64    32               53  69               13  17            35  46
+//                  48               72  72               14  18            47  48
+//                  64               94  72               15  19            59  50
+//   head_dim 128   32               72 123               15  21            49  68
+//                  48              101 127               17  23            67  68
+//                  64              131 129               19  24            84  70
+//   head_dim 256   32              155 176               20  26           104 126
+//                  48              225 180               23  29           148 130
+//                  64              294 181               28  30           193 131
+// Set where long contexts of 64 and 128 change sides; those of 256 would before,
+// short ones of any size later. Both kernels take any number.
 constexpr int kSplitMostRows = 48;
 constexpr int kStages = 2;  // a warp's own work on a tile covers the latency of the next
 constexpr int kTile = 32;   // keys, as two halves of 16: no half crosses a page
@@ -160,7 +171,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int rows_per_gro
 // units of one (KV head, row group): those that stand for what a piece of it
 // costs besides its tiles (rows in, warps joined, results out), then its tiles;
 // one at least, which writes the zeros of a sequence without keys
-// us with 0, 1, 2, 4: 64 sequences up to 16,384 74.5, 70.1, 69.4, 74.0; 8 of 6
+// us with 0, 1, 2, 4 (head_dim 128): 64 sequences up to 16,384 74.5, 70.1, 69.4, 74.0; 8 of 6
 // tokens up to 32,768 58.6, 55.1, 53.6, 53.3; 64 up to 1,500 23, 20, 20, 21.7.
 constexpr int kSplitHead = 2;
 __device__ __forceinline__ int seq_units(const Seq &s) { return kSplitHead + max((s.tiles + kSplitWarps - 1) / kSplitWarps, 1); }

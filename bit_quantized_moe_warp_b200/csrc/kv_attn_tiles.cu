@@ -28,11 +28,13 @@
 // cut into 148 equal runs, one for each CTA; pieces of an item that several CTAs share go through k_attn_join_planes.
 //
 // Measured (B200): 8,192 tokens of 32 heads of 128, the last of 32,768 (4 KV
-// heads): 4.52 ms, 851 TFLOP/s. A step of 256 rows and 128 keys takes about
-// 5,000 cycles, of which the tensor cores work 2,080 (ncu: 28 % of all cycles in
-// a smaller call) and the exponentials need 2,048: a chain of product, wait,
-// softmax (2,500 for a half, two halves at once), wait and product, with two
-// halves in flight. Tensor memory has no room for a third. What was tried:
+// heads): 4.52 ms, 851 TFLOP/s; head_dim 64 3.65 ms, 528 TFLOP/s; 256 14.0 ms,
+// 549 TFLOP/s. At 128 a step of 256 rows and 128 keys takes about 5,000 cycles, of
+// which the tensor cores work 2,080 (ncu: 32 % of all cycles for 2,048 tokens at
+// 8,192) and the exponentials need 2,048: a chain of product, wait, softmax (2,500
+// for a half, two halves at once), wait and product, with two halves in flight.
+// Tensor memory has no room for a third. At the launch's 96 registers ptxas
+// spills 336 bytes of stores and 624 of loads a thread. What was tried:
 //   scores 64 keys at a time in four S, so that products of a half overlap its
 //     softmax: 436 us against 400 (2,048 tokens at 8,192), a product of 64 columns
 //     reads the query rows twice as often;
@@ -233,7 +235,7 @@ STRATA_DEV Item item_of(const AttnArgs &a, const SeqBase &s, int rt) {
 // Units of an item: those that stand for what a piece of it costs besides its
 // tiles (rows in, results out), then its tiles; one at least, which writes the
 // zeros of rows without keys.
-// us with 0, 3, 6, 10: mixed batch 65, 60, 59, 58; 4 sequences of 512 tokens up to
+// us with 0, 3, 6, 10 (head_dim 128, the first 64): mixed batch 65, 60, 59, 58; 4 sequences of 512 tokens up to
 // 4,096 118, 114, 109, 120; 8 of 16 up to 16,000 137, 111, 89, 89; 3 of 1,500 with
 // a window of 512 146, 124, 134, 141.
 constexpr int kHead = 8;

@@ -129,12 +129,15 @@ enum { kPlain, kHalfWhole, kInterleaved, kHalfChunks, kOther };
 
 // One block takes tokens_per_block tokens: their cosines and sines once
 // (fp64) into shared memory, while the first rows are on their way, then the key
-// rows and the value rows of each (in this order, so that warps agree). Bound by
-// instruction issue: 7 butterflies, rotary and rounding of every value; values
+// rows and the value rows of each (in this order, so that warps agree). Values
 // go in pairs where the operation has a form for two. Measured: 8,192 tokens of
-// 4 heads of 128 14.3 us (1.5 TB/s, 37 instructions a value, issue 57 %), without
-// rotary 12.1 us; 64 tokens 7.7 us a call, the call's own cost. At 64 registers
-// and 4 blocks for an SM: 16.5 us.
+// 4 heads of 128 14.4 us (1.5 TB/s, 35 instructions a value, issue active 65 %),
+// without rotary 11.7 us; 64 tokens 7.7 us a call, the call's own cost. Exact
+// rounding is not what bounds it: strata_kv4_encode, with the same bits, takes
+// 8.6 us for these rows. It divides once a lane instead of once a run, skips the
+// clamp for normal scales and packs codes by byte permutes, none of which is
+// done here, beside this kernel's divisions by the page and the heads. At 64
+// registers and 4 blocks for an SM: 16.5 us.
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__ RopeTable tab,
                                                         const __grid_constant__ AppendArgs a) {

@@ -11,7 +11,9 @@
 // memory and serve every head; those of the block's next tokens are computed while
 // this one's chunks stream, and a chunk is fetched while the one before is turned.
 // Measured: 8,192 tokens of 36 heads of 128 30.8 us (4.9 TB/s), 64 tokens 6.8 us a
-// call, the call's own cost.
+// call, the call's own cost. Interleaved 34.9 us (one chunk in flight a thread,
+// where the half layout has two), half of the head turned 37.1 us. Widths that
+// fill no chunk go value by value: 20 of 128 113 us.
 #include <cmath>
 #include <new>
 
