@@ -239,3 +239,23 @@ def test_a_page_in_many_tables_and_twice_in_one(q_len):
     c.check()
     c.cache = S().Kv4Cache(*(t.view(t.shape) for t in c.cache.tensors))
     c.check()
+
+
+@pytest.mark.parametrize("q_len", [1, 70])
+def test_table_without_pages_and_batch_without_sequences(q_len):
+    """A block table of no columns leaves every query without keys; no sequences leave every row as it was."""
+    dev = torch_dev()
+    c = Case([(q_len, 40), (q_len, 20)], 8, 2, 128, 16)
+    c.table = c.table[:, :0].contiguous()
+    out = torch.full_like(c.q, 7.5, memory_format=torch.contiguous_format)
+    assert bool((c.run(out) == 0).all())
+    c.offsets, c.lens, c.table = c.offsets[:1], c.lens[:0], c.table[:0]
+    out.fill_(7.5)
+    assert bool((c.run(out) == 7.5).all())
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_many_query_heads_of_one_kv_head(D, q_len):
+    """300 query heads: a token's rows fill more than one item."""
+    Case([(q_len, 700), (q_len, 33)], 300, 1, D, 16, rope=(D, "half", "none", 1.0), seed=D).check()
